@@ -1,0 +1,197 @@
+// Shared by the expert operators' kernels and their host code (gfx950,
+// wave64): element types, activations, the search of a row tile among the
+// experts, and the launchers (each defined next to its kernels).
+#pragma once
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <cstddef>
+
+#include "lapsum_device.h"
+
+namespace lapsum {
+
+enum Dtype : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
+enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+constexpr int kExpertsMax = 1024;
+constexpr int kSlotsMax = 64;
+
+// rows of dz that one workgroup sums for the bias gradient
+constexpr int kDzRows = 64;
+
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+// workgroups of a launch: kernels walk on by the grid where there is more work
+// (a grid holds fewer than 2^32 threads)
+constexpr long long kGridMax = 1 << 22;
+inline unsigned grid_of(long long n) { return (unsigned)(n < kGridMax ? n : kGridMax); }
+inline size_t dtype_size(int d) { return d == kF32 ? 4 : 2; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// calls f with a value of the element type
+template <class F>
+inline void with_dtype(int d, F&& f) {
+    if (d == kF32) f(float{});
+    else if (d == kBF16) f(__bf16{});
+    else f(_Float16{});
+}
+
+// lapsum_route.hip
+// sums (null: no normalization): per row the sum that the weights are divided by
+void launch_expert_topk(const float* gates, long long T, int E, int m, float floor, int32_t* ids, float* w,
+                        float* sums, hipStream_t st);
+void launch_expert_topk_vjp(const int32_t* ids, const float* w, const float* dw, const float* sums, long long T,
+                            int E, int m, float* dgates, hipStream_t st);
+size_t expert_sort_scratch(long long P, int E);
+void launch_expert_sort(const int32_t* ids, long long P, int E, int32_t* offsets, int32_t* order, int32_t* place,
+                        uint32_t* scratch, hipStream_t st);
+
+// lapsum_tokens.hip
+void launch_dispatch(const void* x, int dtype, long long T, int m, long long D, int E, const int32_t* offsets,
+                     const int32_t* place, void* xs, hipStream_t st);
+void launch_dispatch_vjp(const void* dxs, int dtype, long long T, int m, long long D, const int32_t* place, void* dx,
+                         hipStream_t st);
+void launch_combine(const void* ys, const float* w, const void* residual, int dtype, long long T, int m, long long D,
+                    const int32_t* place, void* out, hipStream_t st);
+void launch_combine_vjp(const void* ys, const float* w, const void* dout, int dtype, long long T, int m, long long D,
+                        int E, const int32_t* offsets, const int32_t* place, void* dys, float* dw, hipStream_t st);
+
+// lapsum_expert_linear.hip
+// One product over all experts.  kFormY: C[rows, out] = A[rows, in] W_e^T;
+// kFormDx: C[rows, in] = A[rows, out] W_e; kFormDw: C_e[out, in] = A^T B over
+// the rows of e (A = dz[rows, out], B = xs[rows, in]).
+enum Form : int { kFormY = 0, kFormDx = 1, kFormDw = 2 };
+struct LinearArgs {
+    const void* a;
+    const void* b;
+    const void* bias;   // kFormY, may be null
+    void* c;
+    void* z;            // kFormY, may be null
+    const int32_t* off;
+    int P, E, in, out;
+    int act;            // kFormY
+};
+void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t st);
+// dz (may be null: dz = dy, not written) and per-chunk column sums (may be
+// null) of dz; then the sums per expert
+void launch_expert_dz(const void* z, const void* dy, int dtype, int act, const int32_t* off, int P, int E, int out,
+                      void* dz, float* part, hipStream_t st);
+void launch_expert_dbias(const float* part, int dtype, const int32_t* off, int P, int E, int out, void* dbias,
+                         hipStream_t st);
+
+#if defined(__HIPCC__)
+
+LS_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+LS_DEV float wave_sum_f32(float v) {
+    v += __uint_as_float(xor_lane<32>(__float_as_uint(v)));
+    v += __uint_as_float(xor_lane<16>(__float_as_uint(v)));
+    v += __uint_as_float(xor_lane<8>(__float_as_uint(v)));
+    v += __uint_as_float(xor_lane<4>(__float_as_uint(v)));
+    v += __uint_as_float(xor_lane<2>(__float_as_uint(v)));
+    v += __uint_as_float(xor_lane<1>(__float_as_uint(v)));
+    return v;
+}
+
+// offsets[e] as a row number: a plan from elsewhere is kept in bounds
+LS_DEV int row_at(const int32_t* __restrict__ off, int e, int P) { return min(max(off[e], 0), P); }
+
+// Tile `tile` of the rows cut into tiles of BM that never cross an expert:
+// its expert and rows [lo, hi).  Behind the last expert's tiles come those of
+// the unused rows (e = E).  `first` is the expert's first tile.  A tile past
+// the end has lo = hi = P.  Every lane of the wave calls it with one `tile`.
+struct RowTile {
+    int e, lo, hi, first;
+};
+template <int BM>
+LS_DEV RowTile find_row_tile(const int32_t* __restrict__ off, int E, int P, int tile) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane_id();
+        int lo = 0, n = 0;
+        if (e < E) {
+            lo = row_at(off, e, P);
+            n = (max(row_at(off, e + 1, P) - lo, 0) + BM - 1) / BM;
+        }
+        const int inc = (int)wave_inclusive_scan((uint32_t)n);
+        const unsigned long long hit = __ballot(base + inc > tile);
+        if (hit) {
+            const int f = __builtin_ctzll(hit);
+            const int first = base + __builtin_amdgcn_readlane(inc, f) - __builtin_amdgcn_readlane(n, f);
+            const int r0 = __builtin_amdgcn_readlane(lo, f) + (tile - first) * BM;
+            const int r1 = uniform(row_at(off, e0 + f + 1, P));
+            return {e0 + f, r0, min(r0 + BM, r1), first};
+        }
+        base += __builtin_amdgcn_readlane(inc, 63);
+    }
+    const long long r0 = (long long)uniform(row_at(off, E, P)) + (long long)(tile - base) * BM;
+    const int lo = (int)min(r0, (long long)P);
+    return {E, lo, min(lo + BM, P), base};
+}
+// number of tiles of the experts and of the unused rows
+template <int BM>
+LS_DEV int count_row_tiles(const int32_t* __restrict__ off, int E, int P) {
+    int n = 0;
+    for (int e = lane_id(); e < E; e += 64) n += (max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + BM - 1) / BM;
+    n = __builtin_amdgcn_readlane((int)wave_inclusive_scan((uint32_t)n), 63);
+    return n + (P - uniform(row_at(off, E, P)) + BM - 1) / BM;
+}
+// most tiles there can be (host)
+template <int BM>
+inline long long max_row_tiles(long long P, int E) {
+    return P / BM + E + 1;
+}
+
+template <class T>
+LS_DEV float to_f(T v) {
+    return (float)v;
+}
+template <class T>
+LS_DEV T from_f(float v) {
+    return (T)v;
+}
+
+// activations and their slopes, in fp32.  e^-z of very negative z is inf and
+// the quotient 0, as it should be
+template <int ACT>
+LS_DEV float act_of(float z) {
+    if (ACT == kActRelu) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if (ACT == kActSilu) return z / (1.0f + __expf(-z));
+    if (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    return z;
+}
+template <int ACT>
+LS_DEV float slope_of(float z) {
+    if (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
+    if (ACT == kActSilu) {
+        const float q = 1.0f / (1.0f + __expf(-z));
+        return q * (1.0f + z * (1.0f - q));
+    }
+    if (ACT == kActGelu)
+        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    return 1.0f;
+}
+
+// z as the VJP keeps it: fp32 for fp32 rows, else fp16 clamped to its range
+// (the slopes are 0 or 1 out there) with the sign of the smallest values kept
+// (relu's slope depends on it).  NaN stays NaN.
+template <class T>
+struct ZKeep {
+    using type = _Float16;
+    static LS_DEV _Float16 make(float z) {
+        _Float16 h = (_Float16)fminf(fmaxf(z, -65504.0f), 65504.0f);
+        if (z != z) h = (_Float16)z;
+        if (z > 0.0f && h == (_Float16)0.0f) h = (_Float16)5.9604645e-8f;
+        return h;
+    }
+};
+template <>
+struct ZKeep<float> {
+    using type = float;
+    static LS_DEV float make(float z) { return z; }
+};
+
+#endif  // __HIPCC__
+
+}  // namespace lapsum
