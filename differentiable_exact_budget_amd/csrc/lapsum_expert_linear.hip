@@ -121,17 +121,13 @@ __global__ __launch_bounds__(kAnyThreads) void k_product_any(LinearArgs g, long 
         product_any<T, FORM, ACT>(g, (int)(t / cols), (int)(t % cols), sa, sb);
 }
 
-template <class F>
-static void with_act(int act, F&& f) {
-    if (act == kActRelu) f(std::integral_constant<int, kActRelu>{});
-    else if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
-    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});
-    else f(std::integral_constant<int, kActNone>{});
-}
-
 void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t st) {
     const int N = form == kFormY ? g.out : g.in;
     if (N < 1 || (form == kFormDw ? g.out : g.P) < 1) return;
+    if (expert_mfma_takes(form, dtype, g)) {
+        launch_expert_mfma(form, dtype, g, st);
+        return;
+    }
     const long long cols = ceil_div(N, kAnyTile);
     const long long tiles =
         cols * (form == kFormDw ? ceil_div(g.out, kAnyTile) * g.E : max_row_tiles<kAnyTile>(g.P, g.E));

@@ -38,6 +38,14 @@ inline void with_dtype(int d, F&& f) {
     else f(_Float16{});
 }
 
+template <class F>
+inline void with_act(int act, F&& f) {
+    if (act == kActRelu) f(std::integral_constant<int, kActRelu>{});
+    else if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
+    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});
+    else f(std::integral_constant<int, kActNone>{});
+}
+
 // lapsum_route.hip
 // sums (null: no normalization): per row the sum that the weights are divided by
 void launch_expert_topk(const float* gates, long long T, int E, int m, float floor, int32_t* ids, float* w,
@@ -74,6 +82,9 @@ struct LinearArgs {
     int act;            // kFormY
 };
 void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t st);
+// lapsum_expert_mfma.hip: the products that the 16-bit matrix instructions take
+bool expert_mfma_takes(int form, int dtype, const LinearArgs& g);
+void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st);
 // dz (may be null: dz = dy, not written) and per-chunk column sums (may be
 // null) of dz; then the sums per expert
 void launch_expert_dz(const void* z, const void* dy, int dtype, int act, const int32_t* off, int P, int E, int out,
