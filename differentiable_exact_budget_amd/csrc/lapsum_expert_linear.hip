@@ -109,8 +109,8 @@ LS_DEV void product_any(const LinearArgs& g, int ti, int tj, float (*sa)[kAnyPad
         const long long i = i0 + wi + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3);
         if (i >= M) continue;
         const float v = acc[r] + bj;
-        if (z) z[i * N + j] = ZKeep<T>::make(v);
-        c[i * N + j] = from_f<T>(act_of<ACT>(v));
+        if (z) z[i * N + j] = ZKeep<T>::template make<ACT>(v);
+        c[i * N + j] = from_f<T>(act_of<ACT, T>(v));
     }
 }
 
@@ -175,9 +175,9 @@ LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const
                 PT o;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float zi = (float)zz.v[i];
+                    const float zi = ZKeep<T>::value(zz.v[i]);
                     // relu drops dy where its slope is 0, inf and NaN too
-                    d[i] = ACT == kActRelu ? (zi > 0.0f ? d[i] : 0.0f) : d[i] * slope_of<ACT>(zi);
+                    d[i] = ACT == kActRelu ? (zi > 0.0f ? d[i] : 0.0f) : d[i] * slope_of<ACT, T>(zi);
                     o.v[i] = from_f<T>(d[i]);
                 }
                 *reinterpret_cast<PT*>(dz + at) = o;

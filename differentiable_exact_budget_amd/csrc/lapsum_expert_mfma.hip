@@ -8,22 +8,32 @@
 //   dx = dz W              A = dz  (k contiguous)   B = W^T (j contiguous)
 //   dW = dz^T xs           A = dz^T (i contiguous)  B = xs^T (j contiguous)
 //
-// A workgroup forms a BM x BN tile of C, 64 steps of k at a time.  The steps'
-// operands go from memory to LDS without passing through registers
-// (buffer_load ... lds, 16 bytes a lane), into one of two buffers while the
-// other is multiplied.  Reads out of range return zero, which is all the
-// masking that ragged experts need: a tile's buffer ends with its expert's
-// last row.
+// A workgroup of four waves forms a BM x BN tile of C, each wave a quarter of
+// it: with 256 x 256 a wave holds 128 x 128 fp32 sums in 256 registers, the
+// most there is, so a byte that is brought to LDS is used as often as it can
+// be.  The sum runs in steps of 32 k, one matrix instruction deep.
+//  - Operands go from memory to LDS without passing through registers
+//    (buffer_load ... lds, 16 bytes a lane) into a ring of five buffers.  Two
+//    steps are fetched as one, alternately all of A and all of B, so that the
+//    two halves of a 128-byte line are asked for together, and the loads are
+//    spread evenly between the matrix instructions: a wave that issues many
+//    at once stands still until the memory pipeline has taken them.
+//  - While a step's fragments are multiplied, the next step's are read from
+//    LDS into a second set of registers.
+//  - Reads out of range return zero, which is all the masking that ragged
+//    experts need: a tile's buffer ends with its expert's last row.
 //
-// LDS layout, free of bank conflicts for the fragment reads below:
-//   k contiguous: row i has 64 k = 8 chunks of 16 bytes; chunk c lies at
-//     c ^ (i & 7).  A fragment is one 16-byte read a lane.
-//   own index contiguous: row k has BM (BN) elements; the pair of chunks q
-//     (16 elements) lies at q ^ ((k & 3) | (k >> 3 & 1) << 2).  A fragment is
-//     two transposing 8-byte reads (ds_read_b64_tr_b16).
+// LDS layout of a step, free of bank conflicts for the fragment reads below:
+//   k contiguous: row i has 32 k = 4 chunks of 16 bytes, two rows to a line
+//     of 128; chunk c lies at c ^ fold(line) within its row's half.  A
+//     fragment is one 16-byte read a lane.
+//   own index contiguous: row k has BM (BN) elements; chunk c lies at
+//     c ^ fold(k).  A fragment is two transposing 8-byte reads
+//     (ds_read_b64_tr_b16).
 // A wave's direct-to-LDS store is 64 consecutive chunks, so the permutation
 // is made on the global side: each lane fetches the chunk that belongs at its
-// place.
+// place.  B's fragments come in pairs that share 32 columns such that a lane
+// ends with 8 consecutive columns of a row of C, one 16-byte store.
 #include "lapsum_expert_ops.h"
 
 namespace lapsum {
@@ -37,268 +47,355 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 #define LS_LDS(T) __attribute__((address_space(3))) T
 
-constexpr int kStepK = 64;  // k of one LDS buffer
+constexpr int kStepK = 32;  // k of one LDS buffer
+constexpr int kRing = 5;    // LDS buffers
+constexpr int kProductThreads = 256;
 
 template <class T>
-LS_DEV f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c);
-template <>
-LS_DEV f32x4 mfma16<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
-template <>
-LS_DEV f32x4 mfma16<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                  0);
+LS_DEV f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
+    if constexpr (std::is_same_v<T, __bf16>)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
 }
 
 // 16 bytes a lane from buffer offset `off` to LDS, lane l at `lds` + 16 l.
 // Written as an instruction so that the compiler's counters do not wait for
-// it at the next LDS read: step_barrier does, one step later.  It has no
-// register output.
+// it at the next LDS read: step_barrier does, when the data is wanted.  It
+// has no register output.
 LS_DEV void load_to_lds(u32x4 rsrc, uint32_t off, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %0, %1, 0 offen lds"
         :
-        : "v"(off), "s"(rsrc), "s"(lds)
-        : "memory");
+        : "v"(off), "s"(rsrc), "s"(lds));
 }
 
-// One operand of a tile: R rows (of its own index) by kStepK of k.
-// KFAST: k is contiguous in memory.
-template <int R, bool KFAST, int WAVES>
-struct Operand {
-    static constexpr int kBytes = R * kStepK * 2;
-    static constexpr int kLoads = kBytes / (WAVES * 1024);  // a wave's loads per step
-    static_assert(kLoads * WAVES * 1024 == kBytes, "whole waves of loads");
-
-    const char* base;  // of the tile's first row and k
-    uint32_t rows;     // rows of the tile that exist (KFAST), else its k
-    uint32_t ld;       // bytes between rows of memory
-    uint32_t voff[kLoads];
-    uint32_t kcol;     // KFAST: first k of this lane's chunk
-    uint32_t last;     // else: bytes of the tile's last memory row that exist
-
-    // x: element (0, 0) of the tile; own: rows left (its own index); K: length
-    // of the sum; ld: elements between memory rows
-    template <class T>
-    LS_DEV void init(const T* x, long long own, int K, int ld_) {
-        base = reinterpret_cast<const char*>(x);
-        ld = (uint32_t)ld_ * 2u;
-        const int l = lane_id(), w = uniform(threadIdx.x >> 6);
-        if (KFAST) {
-            rows = (uint32_t)min((long long)R, own);
-            const int c = (l & 7) ^ (l >> 3);
-            kcol = c * 8;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) voff[i] = (uint32_t)((w * kLoads + i) * 8 + (l >> 3)) * ld + c * 16;
-        } else {
-            rows = (uint32_t)K;
-            last = (uint32_t)min((long long)R, own) * 2u;
-            constexpr int kChunks = R / 8;          // chunks of a k row
-            constexpr int kPer = 64 / kChunks;      // k rows of one load
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int k = (w * kLoads + i) * kPer + l / kChunks;
-                const int f = (k & 3) | ((k >> 3) & 1) << 2;
-                voff[i] = (uint32_t)k * ld + (uint32_t)((l % kChunks) ^ (f << 1)) * 16;
-            }
-        }
-    }
-    // issues the loads of k0 .. k0 + 63 into LDS from byte address `lds`
-    LS_DEV void load(uint32_t lds, int k0, int K) const {
-        const int w = uniform(threadIdx.x >> 6);
-        const char* p;
-        uint32_t n;
-        bool on = true;
-        if (KFAST) {
-            p = base + (size_t)k0 * 2;
-            n = rows * ld - (uint32_t)k0 * 2;
-            on = k0 + (int)kcol < K;  // the last step: what follows in memory is the next row
-        } else {
-            p = base + (size_t)k0 * ld;
-            n = (min((uint32_t)kStepK, rows - (uint32_t)k0) - 1u) * ld + last;
-        }
-        const u32x4 rs = {(uint32_t)(uintptr_t)p, (uint32_t)((uintptr_t)p >> 32), n, 0x00020000u};
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            load_to_lds(rs, KFAST ? (on ? voff[i] : 0x80000000u) : voff[i], lds + (w * kLoads + i) * 1024);
-    }
-    // fragment f (16 rows from r0 + 16 f) of k kk * 32 .. + 31: lane l has row
-    // l % 16, k 8 (l / 16) .. + 7
-    static LS_DEV s16x8 frag(const char* lds, int r0, int f, int kk) {
-        const int l = lane_id(), g = l >> 4, i = l & 15;
-        if (KFAST) {
-            const int c = (kk * 4 + g) ^ (i & 7);
-            return *(const s16x8*)(lds + (r0 + f * 16 + i) * 128 + c * 16);
-        }
-        const int s = (i >> 2) | (g & 1) << 2;
-        const char* p = lds + (kk * 32 + g * 8 + (i >> 2)) * (R * 2) + ((((r0 >> 4) + f) ^ s) << 5) + (i & 3) * 8;
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LS_LDS(s16x4)*)p);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LS_LDS(s16x4)*)(p + 4 * R * 2));
-        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-};
-
-// every wave's loads have landed and its reads are done; then the workgroup meets
+// This wave's loads but the last LEFT have landed and its LDS reads are done;
+// then the workgroup meets.
+template <int LEFT>
 LS_DEV void step_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// Tile `t` of `n` such that the workgroups of one XCD (they are dealt out in
-// turn) take neighbouring tiles, which share operands in its L2.  Returns -1
-// past the end; the grid has at least 8 ceil(n / 8) workgroups' worth.
-LS_DEV int xcd_tile(int block, int n) {
-    const int per = (n + 7) >> 3;
-    const int t = (block & 7) * per + (block >> 3);
-    return (block >> 3) < per && t < n ? t : -1;
-}
+// One operand of a tile: R rows (of its own index) by kStepK of k.
+// KFAST: k is contiguous in memory.  PAIRED: fragments 2 j and 2 j + 1 share
+// the rows 32 j .. + 31, row 8 q + 4 (f & 1) + r being row 4 q + r of fragment
+// f; else fragment f has the rows 16 f .. + 15.
+template <int R, bool KFAST, bool PAIRED>
+struct Operand {
+    static constexpr int kBytes = R * kStepK * 2;
+    static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads per step
+    static constexpr int kChunks = R / 8;                           // chunks of a k row (not KFAST)
 
-// BM x BN tile by WM x WN waves
-template <class T, int FORM, int ACT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64) void k_product(LinearArgs g) {
-    constexpr int kWaves = WM * WN;
-    constexpr bool kA = FORM != kFormDw, kB = FORM == kFormY;  // k contiguous?
-    using OpA = Operand<BM, kA, kWaves>;
-    using OpB = Operand<BN, kB, kWaves>;
-    using Z = typename ZKeep<T>::type;
-    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments of a wave
-    constexpr int kGroup = 4;                            // row tiles that walk the columns together
-    constexpr int kBuffer = OpA::kBytes + OpB::kBytes;
-    __shared__ __align__(1024) char lds[2 * kBuffer];
+    const char* base;       // of the tile's first row and k
+    uint32_t rows;          // rows of the tile that exist (KFAST), else its k
+    uint32_t ld;            // bytes between rows of memory
+    uint32_t last;          // not KFAST: bytes of the tile's last memory row that exist
+    uint32_t kcol;          // KFAST: first k of this lane's chunk
+    uint32_t voff[kLoads];  // this lane's offsets
 
-    const int l = lane_id(), w = uniform(threadIdx.x >> 6);
-    const int r0 = w / WN * (BM / WM), c0 = w % WN * (BN / WN);
-    const int N = FORM == kFormY ? g.out : g.in;
-    const int cols = (N + BN - 1) / BN;
-
-    // the tile: rows [0, M) at c, columns [j0, N)
-    const T *a = (const T*)g.a, *b = (const T*)g.b;
-    T* c = (T*)g.c;
-    Z* z = nullptr;
-    const T* bias = nullptr;
-    int M, K, j0, lda, ldb;
-    if (FORM == kFormDw) {
-        const int rows = (g.out + BM - 1) / BM, per = rows * cols;
-        const int t = xcd_tile(blockIdx.x, per * g.E);
-        if (t < 0) return;
-        const int e = t / per, q = t % per;
-        const int grp = q / (kGroup * cols), first = grp * kGroup, n = min(kGroup, rows - first);
-        const int in = q - first * cols, i0 = (first + in % n) * BM;
-        j0 = in / n * BN;
-        const int lo = uniform(row_at(g.off, e, g.P));
-        K = max(uniform(row_at(g.off, e + 1, g.P)) - lo, 0);
-        M = g.out - i0, lda = g.out, ldb = g.in;
-        a += (long long)lo * lda + i0;
-        b += (long long)lo * ldb;
-        c += ((long long)e * g.out + i0) * g.in;
-    } else {
-        const int t = xcd_tile(blockIdx.x, count_row_tiles<BM>(g.off, g.E, g.P) * cols);
-        if (t < 0) return;
-        // the expert whose tiles hold t / cols, then the place among its tiles
-        const RowTile at = find_row_tile<BM>(g.off, g.E, g.P, t / cols);
-        const int lo = uniform(row_at(g.off, at.e, g.P));
-        const int hi = at.e < g.E ? max(uniform(row_at(g.off, at.e + 1, g.P)), lo) : g.P;
-        const int rows = (hi - lo + BM - 1) / BM, q = t - at.first * cols;
-        const int grp = q / (kGroup * cols), first = grp * kGroup, n = min(kGroup, rows - first);
-        const int in = q - first * cols, i0 = lo + (first + in % n) * BM;
-        j0 = in / n * BN;
-        M = hi - i0;
-        K = FORM == kFormY ? g.in : g.out;
-        lda = K, ldb = g.in;
-        a += (long long)i0 * lda;
-        c += (long long)i0 * N;
-        if (at.e < g.E) {
-            b += (long long)at.e * g.out * g.in;
-            if (FORM == kFormY && g.bias) bias = (const T*)g.bias + (long long)at.e * g.out;
-            if (FORM == kFormY && g.z) z = (Z*)g.z + (long long)i0 * N;
+    static LS_DEV int fold(int q) {
+        if (KFAST) return PAIRED ? (q & 1) | (q >> 1 & 2) : q & 3;
+        return (q & 3) << (PAIRED ? 2 : 1);
+    }
+    // x: element (0, 0) of the tile; own: rows left of its own index; K:
+    // length of the sum; ld_: elements between memory rows
+    template <class T>
+    LS_DEV void init(const T* x, int own, int K, int ld_) {
+        base = reinterpret_cast<const char*>(x);
+        ld = (uint32_t)ld_ * 2u;
+        const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+        if (KFAST) {
+            rows = (uint32_t)min(R, own);
+            const int u = (l & 7) ^ fold(l >> 3), c = u & 3;
+            kcol = c * 8;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                voff[i] = (uint32_t)((w * kLoads + i) * 16 + (l >> 3) * 2 + (u >> 2)) * ld + c * 16;
         } else {
-            K = 0;
+            rows = (uint32_t)K;
+            last = (uint32_t)min(R, own) * 2u;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int k = (w * kLoads + i) * (64 / kChunks) + l / kChunks;
+                voff[i] = (uint32_t)k * ld + (uint32_t)((l % kChunks) ^ fold(k)) * 16;
+            }
         }
     }
-    b += FORM == kFormY ? (long long)j0 * ldb : j0;
+    // the buffer of k0 .. k0 + 31 (empty past K: its loads write zeros)
+    LS_DEV u32x4 window(int k0, int K) const {
+        const char* p = base + (KFAST ? (size_t)k0 * 2 : (size_t)k0 * ld);
+        uint32_t n = KFAST ? rows * ld - (uint32_t)k0 * 2
+                           : (min((uint32_t)kStepK, rows - (uint32_t)k0) - 1u) * ld + last;
+        if (k0 >= K) n = 0;
+        return u32x4{(uint32_t)(uintptr_t)p, (uint32_t)((uintptr_t)p >> 32), n, 0x00020000u};
+    }
+    // issues load i of the window into the LDS buffer at byte address `lds`
+    LS_DEV void load(const u32x4& win, uint32_t lds, int i, int k0, int K) const {
+        const int w = uniform(threadIdx.x >> 6);
+        // the last step of a sum: what follows in memory is the next row
+        const uint32_t off = KFAST && k0 + (int)kcol >= K ? 0x80000000u : voff[i];
+        load_to_lds(win, off, lds + (w * kLoads + i) * 1024);
+    }
+    // fragment f of the rows from r0: lane l has row l % 16 of it, k 8 (l / 16) .. + 7
+    static LS_DEV s16x8 frag(const char* lds, int r0, int f) {
+        const int l = lane_id(), g = l >> 4, i = l & 15;
+        if (KFAST) {
+            const int r = PAIRED ? (f >> 1) * 32 + (i >> 2) * 8 + (f & 1) * 4 + (i & 3) : f * 16 + i;
+            const int u = ((i & 1) * 4 + g) ^ fold(r >> 1 & 7);
+            return *(const s16x8*)(lds + ((r0 + r) >> 1) * 128 + u * 16);
+        }
+        // the read gives lane l column l % 16 of 16, taken 4 columns at a time
+        // from the places that lanes 4 q + b name: row q, block b
+        // (r0 is a multiple of 64, so the fold changes nothing above a
+        // fragment's own bits, and four addresses serve all fragments)
+        const int k = g * 8 + (i >> 2), b = i & 3;
+        const int c = PAIRED ? ((r0 >> 3) + b) ^ fold(k) ^ (f >> 1) << 2
+                             : (r0 >> 3) + ((f & 3) * 2 + (b >> 1) ^ fold(k)) + (f >> 2) * 8;
+        const char* p = lds + k * (R * 2) + c * 16 + (PAIRED ? f & 1 : b & 1) * 8;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LS_LDS(s16x4)*)p);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LS_LDS(s16x4)*)(p + 4 * R * 2));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// What a tile is cut from: A's and B's element (0, 0), C's row 0, the rows
+// and columns left, and the length of the sum.
+template <class T>
+struct Piece {
+    const T *a, *b, *bias;
+    T* c;
+    typename ZKeep<T>::type* z;
+    int M, N, K, lda, ldb, ldc;
+};
+
+// BM x BN of a piece, from its row i0 and column j0
+template <class T, int FORM, int ACT, int BM, int BN>
+LS_DEV void form_tile(const Piece<T>& p, int i0, int j0, char* lds) {
+    constexpr bool kA = FORM != kFormDw, kB = FORM == kFormY;  // k contiguous?
+    using OpA = Operand<BM, kA, false>;
+    using OpB = Operand<BN, kB, true>;
+    using Z = typename ZKeep<T>::type;
+    constexpr int FM = BM / 32, FN = BN / 32;  // fragments of a wave
+    constexpr int kBuffer = OpA::kBytes + OpB::kBytes;
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+    const int r0 = (w >> 1) * (BM / 2), c0 = (w & 1) * (BN / 2);
+    const int M = p.M - i0, N = p.N - j0, K = p.K;
 
     f32x4 acc[FM][FN] = {};
     if (K > 0) {
         OpA oa;
         OpB ob;
-        oa.init(a, M, K, lda);
-        ob.init(b, N - j0, K, ldb);
+        oa.init(p.a + (kA ? (long long)i0 * p.lda : i0), M, K, p.lda);
+        ob.init(p.b + (kB ? (long long)j0 * p.ldb : j0), N, K, p.ldb);
         const uint32_t at = (uint32_t)(uintptr_t)(LS_LDS(char)*)lds;
-        oa.load(at, 0, K);
-        ob.load(at + OpA::kBytes, 0, K);
-        int buf = 0;
-        for (int k0 = 0; k0 < K; k0 += kStepK) {
-            step_barrier();
-            if (k0 + kStepK < K) {
-                const uint32_t to = at + (kBuffer - buf);
-                oa.load(to, k0 + kStepK, K);
-                ob.load(to + OpA::kBytes, k0 + kStepK, K);
+        // steps s and s + 1 of one operand, interleaved, loads [from, to)
+        auto fetch = [&](const auto& op, const u32x4 (&win)[2], int k0, uint32_t to0, uint32_t to1, int from, int to) {
+#pragma unroll
+            for (int r = from; r < to; ++r) {
+                if (r & 1) op.load(win[1], to1, r >> 1, k0 + kStepK, K);
+                else op.load(win[0], to0, r >> 1, k0, K);
             }
-            const char *sa = lds + buf, *sb = sa + OpA::kBytes;
+        };
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                s16x8 fa[FM], fb[FN];
-#pragma unroll
-                for (int j = 0; j < FN; ++j) fb[j] = OpB::frag(sb, c0, j, kk);
-#pragma unroll
-                for (int i = 0; i < FM; ++i) fa[i] = OpA::frag(sa, r0, i, kk);
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<T>(fb[j], fa[i], acc[i][j]);
-            }
-            buf = kBuffer - buf;
+        for (int q = 0; q < 4; q += 2) {
+            const int k0 = q * kStepK;
+            const u32x4 wa[2] = {oa.window(k0, K), oa.window(k0 + kStepK, K)};
+            const u32x4 wb[2] = {ob.window(k0, K), ob.window(k0 + kStepK, K)};
+            const uint32_t to = at + q * kBuffer;
+            fetch(oa, wa, k0, to, to + kBuffer, 0, 2 * OpA::kLoads);
+            fetch(ob, wb, k0, to + OpA::kBytes, to + OpA::kBytes + kBuffer, 0, 2 * OpB::kLoads);
         }
+        s16x8 fa[2][FM], fb[2][FN];
+        step_barrier<2 * (OpA::kLoads + OpB::kLoads)>();
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[0][j] = OpB::frag(lds + OpA::kBytes, c0, j);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[0][i] = OpA::frag(lds, r0, i);
+        // the buffers of steps s - 2, s - 1, s and s + 1
+        int prev2 = 0, prev = 4 * kBuffer, cur = 0, next = kBuffer;
+        // Step s multiplies the fragments of set s % 2 and reads step s + 1
+        // into the other.  An even step fetches A for s + 4 and s + 5, an odd
+        // one B for s + 3 and s + 4, into the two buffers whose fragments are
+        // all read.  An odd step waits for everything before the even step's
+        // loads: the buffers that it and the following step read.
+        auto step = [&](auto qv, int k0) {
+            constexpr int q = decltype(qv)::value;
+            step_barrier<q == 0 ? 63 : 2 * OpA::kLoads>();
+            const char *sa = lds + next, *sb = sa + OpA::kBytes;
+            constexpr int kReads = FM + FN, kReadIn = FM / 2;
+            const int kf = k0 + (q == 0 ? 4 : 3) * kStepK;
+            u32x4 win[2];
+            if (q == 0) win[0] = oa.window(kf, K), win[1] = oa.window(kf + kStepK, K);
+            else win[0] = ob.window(kf, K), win[1] = ob.window(kf + kStepK, K);
+            const uint32_t to0 = at + (q == 0 ? prev : prev2 + OpA::kBytes);
+            const uint32_t to1 = at + (q == 0 ? cur : prev + OpA::kBytes);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                if (i < kReadIn) {
+#pragma unroll
+                    for (int r = i * kReads / kReadIn; r < (i + 1) * kReads / kReadIn; ++r) {
+                        if (r < FN) fb[q ^ 1][r] = OpB::frag(sb, c0, r);
+                        else fa[q ^ 1][r - FN] = OpA::frag(sa, r0, r - FN);
+                    }
+                }
+                if (q == 0) fetch(oa, win, kf, to0, to1, i * 2 * OpA::kLoads / FM, (i + 1) * 2 * OpA::kLoads / FM);
+                else fetch(ob, win, kf, to0, to1, i * 2 * OpB::kLoads / FM, (i + 1) * 2 * OpB::kLoads / FM);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<T>(fb[q][j], fa[q][i], acc[i][j]);
+                // keeps the compiler from gathering the loads
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            prev2 = prev;
+            prev = cur;
+            cur = next;
+            next = next == (kRing - 1) * kBuffer ? 0 : next + kBuffer;
+        };
+        for (int k0 = 0; k0 < K; k0 += 2 * kStepK) {
+            step(std::integral_constant<int, 0>{}, k0);
+            step(std::integral_constant<int, 1>{}, k0 + kStepK);
+        }
+        // nothing may land in LDS after this, or in registers' stead
+        step_barrier<0>();
     }
-    // lane l holds row l % 16 of a fragment, columns 4 (l / 16) .. + 3
-    struct __attribute__((aligned(8))) T4 { T v[4]; };
-    struct __attribute__((aligned(8))) Z4 { Z v[4]; };
+    // lane l holds row l % 16 of a fragment and, of a pair of fragments,
+    // columns 8 (l / 16) .. + 7
+    struct __attribute__((aligned(16))) T8 { T v[8]; };
+    struct __attribute__((aligned(16))) Z8 { Z v[8]; };
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int col = j0 + c0 + j * 16 + (l >> 4) * 4;
+    for (int j = 0; j < FN; j += 2) {
+        const int col = c0 + j * 16 + (l >> 4) * 8;
         if (col >= N) continue;
-        float bj[4] = {};
-        if (FORM == kFormY && bias) {
-            const T4 v = *(const T4*)(bias + col);
+        float bj[8] = {};
+        if (FORM == kFormY && p.bias) {
+            const T8 v = *(const T8*)(p.bias + j0 + col);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) bj[r] = to_f(v.v[r]);
+            for (int r = 0; r < 8; ++r) bj[r] = to_f(v.v[r]);
         }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int row = r0 + i * 16 + (l & 15);
             if (row >= M) continue;
-            T4 o;
-            Z4 k;
+            const long long to = (long long)(i0 + row) * p.ldc + j0 + col;
+            T8 o;
+            Z8 k;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float v = acc[i][j][r] + bj[r];
-                if (FORM == kFormY && ACT != kActNone) k.v[r] = ZKeep<T>::make(v);
-                o.v[r] = from_f<T>(act_of<ACT>(v));
+            for (int r = 0; r < 8; ++r) {
+                const float v = acc[i][j + (r >> 2)][r & 3] + bj[r];
+                if (FORM == kFormY && ACT != kActNone) k.v[r] = ZKeep<T>::template make<ACT>(v);
+                o.v[r] = from_f<T>(act_of<ACT, T>(v));
             }
-            *(T4*)(c + (long long)row * N + col) = o;
-            if (FORM == kFormY && ACT != kActNone && z) *(Z4*)(z + (long long)row * N + col) = k;
+            *(T8*)(p.c + to) = o;
+            if (FORM == kFormY && ACT != kActNone && p.z)  // not read before the backward pass
+                __builtin_nontemporal_store(__builtin_bit_cast(u32x4, k), (u32x4*)(p.z + to));
         }
     }
 }
 
-template <class T, int BM, int BN, int WM, int WN>
+// Which tile a workgroup forms.  Workgroups are dealt out to the eight XCDs
+// in turn; 32 at a time (one per CU) an XCD takes neighbouring tiles, which
+// share operands in its L2, and the XCDs' 32 follow one another, so that
+// together they walk one expert or two at a time and what one XCD fetches the
+// others find in the memory-side cache.  Tiles past the last whole round of
+// 256 are cut into quarters when that fills the CUs better: a quarter takes
+// about a third of a tile's time, so up to 128 of them are worth it.
+constexpr int kXcds = 8, kXcdTiles = 32, kRound = kXcds * kXcdTiles;
+constexpr int kCutTiles = 128;
+struct Turn {
+    int tile;     // -1: none
+    int quarter;  // 0 .. 3, or -1: the whole tile
+};
+LS_DEV Turn take_turn(int block, int n, bool cut) {
+    const int full = n / kRound * kRound;
+    const int x = block % kXcds, i = block / kXcds;
+    if (block < full) return {(i / kXcdTiles * kXcds + x) * kXcdTiles + i % kXcdTiles, -1};
+    const int rest = n - full, r = i - full / kXcds;
+    cut = cut && rest <= kCutTiles;
+    const int work = cut ? rest * 4 : rest, per = (work + kXcds - 1) / kXcds, t = x * per + r;
+    if (r >= per || t >= work) return {-1, -1};
+    return cut ? Turn{full + t / 4, t & 3} : Turn{full + t, -1};
+}
+inline long long turns(long long n, bool cut) { return ceil_div(n + (cut ? 3 * kCutTiles : 0), kXcds) * kXcds + kXcds; }
+
+template <class T, int FORM, int ACT, int BM, int BN>
+__global__ __launch_bounds__(kProductThreads) void k_product(LinearArgs g) {
+    constexpr int kGroup = 4;  // row tiles that walk the columns together: 4 x 8 tiles on an XCD at a time
+    constexpr bool kCut = BM == 256;
+    __shared__ __align__(1024) char lds[kRing * (BM + BN) * kStepK * 2];
+    Piece<T> p;
+    p.N = FORM == kFormY ? g.out : g.in;
+    p.ldc = p.N;
+    p.bias = nullptr;
+    p.z = nullptr;
+    const int cols = (p.N + BN - 1) / BN;
+    int q, rows, quarter;  // tile of the expert, its row tiles
+    if (FORM == kFormDw) {
+        rows = (g.out + BM - 1) / BM;
+        const Turn t = take_turn(blockIdx.x, rows * cols * g.E, kCut);
+        if (t.tile < 0) return;
+        const int e = t.tile / (rows * cols);
+        q = t.tile % (rows * cols);
+        quarter = t.quarter;
+        const int lo = uniform(row_at(g.off, e, g.P));
+        p.K = max(uniform(row_at(g.off, e + 1, g.P)) - lo, 0);
+        p.M = g.out, p.lda = g.out, p.ldb = g.in;
+        p.a = (const T*)g.a + (long long)lo * g.out;
+        p.b = (const T*)g.b + (long long)lo * g.in;
+        p.c = (T*)g.c + (long long)e * g.out * g.in;
+    } else {
+        const Turn t = take_turn(blockIdx.x, count_row_tiles<BM>(g.off, g.E, g.P) * cols, kCut);
+        if (t.tile < 0) return;
+        const RowTile at = find_row_tile<BM>(g.off, g.E, g.P, t.tile / cols);
+        const int lo = uniform(row_at(g.off, at.e, g.P));
+        const int hi = at.e < g.E ? max(uniform(row_at(g.off, at.e + 1, g.P)), lo) : g.P;
+        p.M = hi - lo;
+        rows = (p.M + BM - 1) / BM;
+        q = t.tile - at.first * cols;
+        quarter = t.quarter;
+        p.K = at.e == g.E ? 0 : FORM == kFormY ? g.in : g.out;  // unused rows: zeros
+        p.lda = FORM == kFormY ? g.in : g.out;
+        p.ldb = g.in;
+        p.a = (const T*)g.a + (long long)lo * p.lda;
+        p.b = (const T*)g.b + (long long)(at.e < g.E ? at.e : 0) * g.out * g.in;
+        p.c = (T*)g.c + (long long)lo * p.N;
+        if (FORM == kFormY && at.e < g.E) {
+            if (g.bias) p.bias = (const T*)g.bias + (long long)at.e * g.out;
+            if (g.z) p.z = (typename ZKeep<T>::type*)g.z + (long long)lo * p.N;
+        }
+    }
+    const int first = q / (kGroup * cols) * kGroup, n = min(kGroup, rows - first);
+    const int in = q - first * cols;
+    int i0 = (first + in % n) * BM, j0 = in / n * BN;
+    if constexpr (kCut) {
+        if (quarter >= 0) {
+            i0 += (quarter >> 1) * (BM / 2);
+            j0 += (quarter & 1) * (BN / 2);
+            if (i0 < p.M && j0 < p.N) form_tile<T, FORM, ACT, BM / 2, BN / 2>(p, i0, j0, lds);
+            return;
+        }
+    }
+    form_tile<T, FORM, ACT, BM, BN>(p, i0, j0, lds);
+}
+
+template <class T, int BM, int BN>
 static void launch_tiles(int form, const LinearArgs& g, hipStream_t st) {
     const int N = form == kFormY ? g.out : g.in;
     const long long cols = ceil_div(N, BN);
     const long long tiles = cols * (form == kFormDw ? ceil_div(g.out, BM) * g.E : max_row_tiles<BM>(g.P, g.E));
-    const dim3 grid((unsigned)(ceil_div(tiles, 8) * 8)), block(WM * WN * 64);
+    const dim3 grid((unsigned)turns(tiles, BM == 256)), block(kProductThreads);
     if (form == kFormDw)
-        hipLaunchKernelGGL((k_product<T, kFormDw, kActNone, BM, BN, WM, WN>), grid, block, 0, st, g);
+        hipLaunchKernelGGL((k_product<T, kFormDw, kActNone, BM, BN>), grid, block, 0, st, g);
     else if (form == kFormDx)
-        hipLaunchKernelGGL((k_product<T, kFormDx, kActNone, BM, BN, WM, WN>), grid, block, 0, st, g);
+        hipLaunchKernelGGL((k_product<T, kFormDx, kActNone, BM, BN>), grid, block, 0, st, g);
     else
         with_act(g.act, [&](auto av) {
-            hipLaunchKernelGGL((k_product<T, kFormY, decltype(av)::value, BM, BN, WM, WN>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((k_product<T, kFormY, decltype(av)::value, BM, BN>), grid, block, 0, st, g);
         });
 }
 
@@ -315,7 +412,7 @@ bool expert_mfma_takes(int form, int dtype, const LinearArgs& g) {
 void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st) {
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
-        if constexpr (sizeof(T) == 2) launch_tiles<T, 256, 256, 2, 4>(form, g, st);
+        if constexpr (sizeof(T) == 2) launch_tiles<T, 256, 256>(form, g, st);
     });
 }
 

@@ -163,44 +163,78 @@ LS_DEV T from_f(float v) {
     return (T)v;
 }
 
-// activations and their slopes, in fp32.  e^-z of very negative z is inf and
-// the quotient 0, as it should be
-template <int ACT>
+// 1 / (1 + e^-z): the hardware exponential and reciprocal, 1 ulp each; e^-z
+// of very negative z is inf and its reciprocal 0, as it should be
+LS_DEV float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+// The normal distribution's tail Q(x) = erfc(x / sqrt 2) / 2 for x >= 0 after
+// Abramowitz and Stegun 7.1.26: a polynomial in 1 / (1 + p x / sqrt 2) times
+// e = e^(-x x / 2); within 1e-7 of Q.
+LS_DEV float normal_tail(float x, float e) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(x, 0.3275911f * 0.70710678f, 1.0f));
+    float s = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    s = fmaf(t, s, 0.5f * 1.421413741f);
+    s = fmaf(t, s, 0.5f * -0.284496736f);
+    s = fmaf(t, s, 0.5f * 0.254829592f);
+    return s * t * e;
+}
+
+// Activations and their slopes, in fp32; T is the rows' type.  For 16-bit
+// rows gelu takes the polynomial tail, whose error is below their rounding.
+template <int ACT, class T>
 LS_DEV float act_of(float z) {
     if (ACT == kActRelu) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    if (ACT == kActSilu) return z / (1.0f + __expf(-z));
-    if (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    if (ACT == kActSilu) return z * sigmoid(z);
+    if (ACT == kActGelu) {
+        if (sizeof(T) == 4) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+        const float q = normal_tail(fabsf(z), __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.4426950408889634f)));
+        return z * (z > 0.0f ? 1.0f - q : q);
+    }
     return z;
 }
-template <int ACT>
+template <int ACT, class T>
 LS_DEV float slope_of(float z) {
     if (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
     if (ACT == kActSilu) {
-        const float q = 1.0f / (1.0f + __expf(-z));
-        return q * (1.0f + z * (1.0f - q));
+        const float q = sigmoid(z);
+        return q * fmaf(z, 1.0f - q, 1.0f);
     }
-    if (ACT == kActGelu)
-        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    if (ACT == kActGelu) {
+        const float e = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.4426950408889634f));
+        if (sizeof(T) == 4) return fmaf(z * 0.39894228f, e, 0.5f * (1.0f + erff(z * 0.70710678f)));
+        const float q = normal_tail(fabsf(z), e);
+        return fmaf(z * 0.39894228f, e, z > 0.0f ? 1.0f - q : q);
+    }
     return 1.0f;
 }
 
-// z as the VJP keeps it: fp32 for fp32 rows, else fp16 clamped to its range
-// (the slopes are 0 or 1 out there) with the sign of the smallest values kept
-// (relu's slope depends on it).  NaN stays NaN.
+// z as the VJP keeps it: fp32 for fp32 rows, else fp16, where a z beyond its
+// range becomes infinite (the VJP takes it as the largest fp16: the slopes
+// are 0 or 1 out there).  relu's slope depends on the sign alone, so a
+// positive z that rounds to 0 is kept as the smallest positive value.
 template <class T>
 struct ZKeep {
     using type = _Float16;
+    template <int ACT>
     static LS_DEV _Float16 make(float z) {
-        _Float16 h = (_Float16)fminf(fmaxf(z, -65504.0f), 65504.0f);
-        if (z != z) h = (_Float16)z;
-        if (z > 0.0f && h == (_Float16)0.0f) h = (_Float16)5.9604645e-8f;
+        const _Float16 h = (_Float16)z;
+        if (ACT == kActRelu && z > 0.0f && h == (_Float16)0.0f) return (_Float16)5.9604645e-8f;
         return h;
+    }
+    static LS_DEV float value(_Float16 h) {
+        const float z = (float)h;
+        return fabsf(z) > 65504.0f ? copysignf(65504.0f, z) : z;
     }
 };
 template <>
 struct ZKeep<float> {
     using type = float;
-    static LS_DEV float make(float z) { return z; }
+    template <int ACT>
+    static LS_DEV float make(float z) {
+        return z;
+    }
+    static LS_DEV float value(float z) { return z; }
 };
 
 #endif  // __HIPCC__

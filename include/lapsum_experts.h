@@ -137,8 +137,8 @@ lapsum_status_t lapsum_expert_combine_vjp(const void* ys, const float* weights, 
  *   ys     : dtype[rows, out].
  *   z_out  : NULL, or fp16 (fp32 for LAPSUM_F32)[rows, out]: z as the VJP
  *            wants it (not written past offsets[experts]).  z is kept in
- *            fp16 whatever the 16-bit type, clamped to its range: only the
- *            activation's slope is taken from it, which is 0 or 1 there.
+ *            fp16 whatever the 16-bit type, infinite beyond its range: only
+ *            the activation's slope is taken from it, which is 0 or 1 there.
  * rows <= LAPSUM_MAX_PAIRS, in and out < 2^31.
  */
 lapsum_status_t lapsum_expert_linear(const void* xs, const void* weight, const void* bias, lapsum_dtype_t dtype,
