@@ -161,29 +161,38 @@ LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const
     const int l = lane_id(), w = threadIdx.x >> 6;
     const long long c = (long long)tj * (64 * V) + l * V;
     float sum[V] = {};
+    // four rows' loads are in flight at a time
+    constexpr int U = 4;
+    struct __attribute__((aligned(sizeof(T) * V))) PT { T v[V]; };
+    struct __attribute__((aligned(sizeof(Z) * V))) PZ { Z v[V]; };
     if (c < N) {
-        for (int r = t.lo + w; r < t.hi; r += 4) {
-            const long long at = (long long)r * N + c;
-            struct __attribute__((aligned(sizeof(T) * V))) PT { T v[V]; };
-            struct __attribute__((aligned(sizeof(Z) * V))) PZ { Z v[V]; };
-            const PT g = *reinterpret_cast<const PT*>(dy + at);
-            float d[V];
+        for (int r0 = t.lo + w; r0 < t.hi; r0 += 4 * U) {
+            PT g[U];
+            PZ z[U];
 #pragma unroll
-            for (int i = 0; i < V; ++i) d[i] = to_f(g.v[i]);
-            if (ACT != kActNone) {
-                const PZ zz = *reinterpret_cast<const PZ*>((const Z*)zp + at);
+            for (int u = 0; u < U; ++u) {
+                const long long at = (long long)min(r0 + 4 * u, t.hi - 1) * N + c;
+                g[u] = *reinterpret_cast<const PT*>(dy + at);
+                if (ACT != kActNone) z[u] = *reinterpret_cast<const PZ*>((const Z*)zp + at);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + 4 * u;
+                if (r >= t.hi) break;
                 PT o;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float zi = ZKeep<T>::value(zz.v[i]);
-                    // relu drops dy where its slope is 0, inf and NaN too
-                    d[i] = ACT == kActRelu ? (zi > 0.0f ? d[i] : 0.0f) : d[i] * slope_of<ACT, T>(zi);
-                    o.v[i] = from_f<T>(d[i]);
+                    float d = to_f(g[u].v[i]);
+                    if (ACT != kActNone) {
+                        const float zi = ZKeep<T>::value(z[u].v[i]);
+                        // relu drops dy where its slope is 0, inf and NaN too
+                        d = ACT == kActRelu ? (zi > 0.0f ? d : 0.0f) : d * slope_of<ACT, T>(zi);
+                        o.v[i] = from_f<T>(d);
+                    }
+                    sum[i] += d;
                 }
-                *reinterpret_cast<PT*>(dz + at) = o;
+                if (ACT != kActNone) *reinterpret_cast<PT*>(dz + (long long)r * N + c) = o;
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] += d[i];
         }
     }
     if (!part) return;
@@ -208,21 +217,29 @@ __global__ __launch_bounds__(256) void k_dz(const void* __restrict__ zp, const T
     }
 }
 
+// An expert's partial sums, 64 columns a workgroup: a wave adds every fourth
+// tile's, eight loads in flight, and the waves' sums are added in wave order.
 template <class T>
-__global__ __launch_bounds__(64) void k_dbias(const float* __restrict__ part, const int32_t* __restrict__ off, int P,
-                                              int E, int N, T* __restrict__ dbias) {
-    const int e = blockIdx.y;
+__global__ __launch_bounds__(256) void k_dbias(const float* __restrict__ part, const int32_t* __restrict__ off, int P,
+                                               int E, int N, T* __restrict__ dbias) {
+    __shared__ float s[4][64];
+    const int e = blockIdx.y, l = lane_id(), w = uniform(threadIdx.x >> 6);
     // the expert's first tile of rows: those of the experts before it
-    int first = 0, n = 0;
-    for (int i = lane_id(); i < e; i += 64)
+    int first = 0;
+    for (int i = l; i < e; i += 64)
         first += (max(row_at(off, i + 1, P) - row_at(off, i, P), 0) + kDzRows - 1) / kDzRows;
     first = __builtin_amdgcn_readlane((int)wave_inclusive_scan((uint32_t)first), 63);
-    n = (max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + kDzRows - 1) / kDzRows;
-    const long long c = (long long)blockIdx.x * 64 + lane_id();
-    if (c >= N) return;
+    const int n = (max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + kDzRows - 1) / kDzRows;
+    const long long c = (long long)blockIdx.x * 64 + l;
     float sum = 0.0f;
-    for (int i = 0; i < n; ++i) sum += part[(long long)(first + i) * N + c];
-    dbias[(long long)e * N + c] = from_f<T>(sum);
+    if (c < N) {
+        const float* p = part + (long long)first * N + c;
+#pragma unroll 8
+        for (int i = w; i < n; i += 4) sum += p[(long long)i * N];
+    }
+    s[w][l] = sum;
+    __syncthreads();
+    if (w == 0 && c < N) dbias[(long long)e * N + c] = from_f<T>((s[0][l] + s[1][l]) + (s[2][l] + s[3][l]));
 }
 
 void launch_expert_dz(const void* z, const void* dy, int dtype, int act, const int32_t* off, int P, int E, int out,
@@ -251,7 +268,7 @@ void launch_expert_dbias(const float* part, int dtype, const int32_t* off, int P
     if (out < 1) return;
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
-        hipLaunchKernelGGL(k_dbias<T>, dim3((unsigned)ceil_div(out, 64), (unsigned)E), dim3(64), 0, st, part, off, P,
+        hipLaunchKernelGGL(k_dbias<T>, dim3((unsigned)ceil_div(out, 64), (unsigned)E), dim3(256), 0, st, part, off, P,
                            E, out, (T*)dbias);
     });
 }

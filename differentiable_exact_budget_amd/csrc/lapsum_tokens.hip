@@ -1,9 +1,16 @@
 // Token rows to their experts' places and back.
 //
-// Every kernel gives a token to one wave: it reads the token's row (or sums
-// into it) and touches the row of each of its slots, so a token's row is read
-// from memory once however many slots it has, and every sum runs in the order
-// of the slots.  They are copies with a little arithmetic: HBM bounds them.
+// Every kernel gives a token, or a stretch of its columns, to one wave: it
+// reads the token's row (or sums into it) and touches the row of each of its
+// slots, so a token's row is read from memory once however many slots it has,
+// and every sum runs in the order of the slots.  They are copies with a
+// little arithmetic: HBM bounds them where there are many tokens, and the
+// latency of one load behind another where there are few.  So a wave keeps
+// several 16-byte loads in flight (U stretches of 64 lanes), and with few
+// tokens a row is spread over many waves instead (U = 1).
+//
+// Rows need not start on 16 bytes: the hardware takes 16-byte loads and stores
+// at any element's address, and only a row's last elements go one by one.
 //
 // A slot's place is read from its lane (readlane) only where the whole wave
 // is active: loops over a row's columns run to the wave's end and mask their
@@ -17,18 +24,40 @@ namespace lapsum {
 constexpr int kTokWaves = 4;
 constexpr int kTokThreads = kTokWaves * 64;
 
-// V elements of a row in one load
-template <class T, int V>
-struct __attribute__((aligned(sizeof(T) * V))) Pack {
+// 16 bytes of a row at any element's address
+template <class T>
+struct Pack {
+    static constexpr int V = 16 / (int)sizeof(T);
     T v[V];
 };
-template <class T, int V>
-LS_DEV Pack<T, V> ld(const T* p) {
-    return *reinterpret_cast<const Pack<T, V>*>(p);
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Loose {
+    Pack<T> p;
+};
+// elements c .. of a row of D elements; past the row's end: zeros
+template <class T>
+LS_DEV Pack<T> ld(const T* row, long long c, long long D) {
+    constexpr int V = Pack<T>::V;
+    Pack<T> x{};
+    if (c + V <= D) {
+        x = reinterpret_cast<const Loose<T>*>(row + c)->p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < D) x.v[i] = row[c + i];
+    }
+    return x;
 }
-template <class T, int V>
-LS_DEV void st(T* p, const Pack<T, V>& x) {
-    *reinterpret_cast<Pack<T, V>*>(p) = x;
+template <class T>
+LS_DEV void st(T* row, long long c, long long D, const Pack<T>& x) {
+    constexpr int V = Pack<T>::V;
+    if (c + V <= D) {
+        reinterpret_cast<Loose<T>*>(row + c)->p = x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < D) row[c + i] = x.v[i];
+    }
 }
 
 // positions of a token's slots, slot j in lane j; -1 for empty ones
@@ -38,139 +67,183 @@ LS_DEV int slot_place(const int32_t* __restrict__ place, long long t, int m, lon
     return (unsigned long long)(long long)pos < (unsigned long long)P ? pos : -1;
 }
 
-// zeros in the rows past offsets[E], dealt out over the tokens' waves
-template <class T, int V>
+// zeros in the columns from c of the rows past offsets[E], dealt out over the
+// tokens
+template <class T, int U>
 LS_DEV void zero_unused(T* __restrict__ rows, const int32_t* __restrict__ off, int E, long long P, long long D,
-                        long long t, long long T_) {
+                        long long t, long long T_, long long c) {
     const long long used = min(max((long long)off[E], 0ll), P);
-    Pack<T, V> z{};
     for (long long r = used + t; r < P; r += T_)
-        for (long long c = (long long)lane_id() * V; c < D; c += 64 * V) st<T, V>(rows + r * D + c, z);
+#pragma unroll
+        for (int u = 0; u < U; ++u) st<T>(rows + r * D, c + u * 64 * Pack<T>::V, D, Pack<T>{});
 }
 
-template <class T, int V>
+// A wave's work: token t, columns from c0.  `stretches` = ceil(D / (64 V U)).
+struct Task {
+    long long t, c0;
+};
+template <class T, int U>
+LS_DEV Task task_of(long long i, int stretches) {
+    const long long t = i / stretches;
+    return {t, (i - t * stretches) * (64 * Pack<T>::V * U)};
+}
+
+template <class T, int U>
 __global__ __launch_bounds__(kTokThreads) void k_dispatch(const T* __restrict__ x, long long T_, int m, long long D,
-                                                           int E, const int32_t* __restrict__ off,
+                                                           int E, int stretches, const int32_t* __restrict__ off,
                                                            const int32_t* __restrict__ place, T* __restrict__ xs) {
-    for (long long t = (long long)blockIdx.x * kTokWaves + uniform(threadIdx.x >> 6); t < T_;
-         t += (long long)gridDim.x * kTokWaves) {
-        const long long P = T_ * m;
-        const int pos = slot_place(place, t, m, P);
-        for (long long c0 = 0; c0 < D; c0 += 64 * V) {
-            const long long c = c0 + lane_id() * V;
-            const bool on = c < D;
-            Pack<T, V> v{};
-            if (on) v = ld<T, V>(x + t * D + c);
-            for (int j = 0; j < m; ++j) {
-                const int p = __builtin_amdgcn_readlane(pos, j);
-                if (p >= 0 && on) st<T, V>(xs + (long long)p * D + c, v);
-            }
+    constexpr int V = Pack<T>::V;
+    const long long P = T_ * m;
+    for (long long i = (long long)blockIdx.x * kTokWaves + uniform(threadIdx.x >> 6); i < T_ * stretches;
+         i += (long long)gridDim.x * kTokWaves) {
+        const Task a = task_of<T, U>(i, stretches);
+        const int pos = slot_place(place, a.t, m, P);
+        const long long c = a.c0 + lane_id() * V;
+        Pack<T> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = ld<T>(x + a.t * D, c + u * 64 * V, D);
+        for (int j = 0; j < m; ++j) {
+            const int p = __builtin_amdgcn_readlane(pos, j);
+            if (p < 0) continue;
+#pragma unroll
+            for (int u = 0; u < U; ++u) st<T>(xs + (long long)p * D, c + u * 64 * V, D, v[u]);
         }
-        zero_unused<T, V>(xs, off, E, P, D, t, T_);
+        zero_unused<T, U>(xs, off, E, P, D, a.t, T_, c);
     }
 }
 
 // out = residual + sum of w rows (weights null: 1)
-template <class T, int V>
+template <class T, int U>
 __global__ __launch_bounds__(kTokThreads) void k_combine(const T* __restrict__ ys, const float* __restrict__ w,
                                                           const T* __restrict__ residual, long long T_, int m,
-                                                          long long D, const int32_t* __restrict__ place,
-                                                          T* __restrict__ out) {
-    for (long long t = (long long)blockIdx.x * kTokWaves + uniform(threadIdx.x >> 6); t < T_;
-         t += (long long)gridDim.x * kTokWaves) {
-        const int l = lane_id();
-        const int pos = slot_place(place, t, m, T_ * m);
-        const float wt = w && l < m ? w[t * m + l] : 1.0f;
-        for (long long c0 = 0; c0 < D; c0 += 64 * V) {
-            const long long c = c0 + l * V;
-            const bool on = c < D;
-            float acc[V] = {};
-            if (residual && on) {
-                const Pack<T, V> v = ld<T, V>(residual + t * D + c);
+                                                          long long D, int stretches,
+                                                          const int32_t* __restrict__ place, T* __restrict__ out) {
+    constexpr int V = Pack<T>::V;
+    const int l = lane_id();
+    for (long long i = (long long)blockIdx.x * kTokWaves + uniform(threadIdx.x >> 6); i < T_ * stretches;
+         i += (long long)gridDim.x * kTokWaves) {
+        const Task a = task_of<T, U>(i, stretches);
+        const int pos = slot_place(place, a.t, m, T_ * m);
+        const float wt = w && l < m ? w[a.t * m + l] : 1.0f;
+        const long long c = a.c0 + l * V;
+        float acc[U][V] = {};
+        if (residual) {
+            Pack<T> v[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = to_f(v.v[i]);
-            }
-            for (int j = 0; j < m; ++j) {
-                const int p = __builtin_amdgcn_readlane(pos, j);
-                if (p < 0) continue;
-                const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wt), j));
-                Pack<T, V> v{};
-                if (on) v = ld<T, V>(ys + (long long)p * D + c);
+            for (int u = 0; u < U; ++u) v[u] = ld<T>(residual + a.t * D, c + u * 64 * V, D);
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, to_f(v.v[i]), acc[i]);
-            }
-            Pack<T, V> o;
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(acc[i]);
-            if (on) st<T, V>(out + t * D + c, o);
+                for (int q = 0; q < V; ++q) acc[u][q] = to_f(v[u].v[q]);
+        }
+        // two slots' rows in flight
+        for (int j = 0; j < m; j += 2) {
+            const int p0 = __builtin_amdgcn_readlane(pos, j), p1 = j + 1 < m ? __builtin_amdgcn_readlane(pos, j + 1) : -1;
+            const float w0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wt), j));
+            const float w1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wt), min(j + 1, m - 1)));
+            Pack<T> v0[U] = {}, v1[U] = {};
+            if (p0 >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u) v0[u] = ld<T>(ys + (long long)p0 * D, c + u * 64 * V, D);
+            if (p1 >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u) v1[u] = ld<T>(ys + (long long)p1 * D, c + u * 64 * V, D);
+            if (p0 >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) acc[u][q] = fmaf(w0, to_f(v0[u].v[q]), acc[u][q]);
+            if (p1 >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) acc[u][q] = fmaf(w1, to_f(v1[u].v[q]), acc[u][q]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pack<T> o;
+#pragma unroll
+            for (int q = 0; q < V; ++q) o.v[q] = from_f<T>(acc[u][q]);
+            st<T>(out + a.t * D, c + u * 64 * V, D, o);
         }
     }
 }
 
-template <class T, int V>
+// A wave takes a whole token (dw is a sum over the row), U stretches at a time.
+template <class T, int U>
 __global__ __launch_bounds__(kTokThreads) void k_combine_vjp(const T* __restrict__ ys, const float* __restrict__ w,
                                                               const T* __restrict__ dout, long long T_, int m,
                                                               long long D, int E, const int32_t* __restrict__ off,
                                                               const int32_t* __restrict__ place, T* __restrict__ dys,
                                                               float* __restrict__ dw) {
+    constexpr int V = Pack<T>::V;
+    const int l = lane_id();
+    const long long P = T_ * m;
     for (long long t = (long long)blockIdx.x * kTokWaves + uniform(threadIdx.x >> 6); t < T_;
          t += (long long)gridDim.x * kTokWaves) {
-        const int l = lane_id();
-        const long long P = T_ * m;
         const int pos = slot_place(place, t, m, P);
         const float wt = l < m ? w[t * m + l] : 0.0f;
-        float mine = 0.0f;
-        for (int j = 0; j < m; ++j) {
-            const int p = __builtin_amdgcn_readlane(pos, j);
-            if (p < 0) continue;
-            const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wt), j));
-            float dot = 0.0f;
-            for (long long c = (long long)l * V; c < D; c += 64 * V) {
-                const Pack<T, V> g = ld<T, V>(dout + t * D + c);
+        float mine = 0.0f;  // slot l's dw
+        for (long long c0 = 0; c0 < D; c0 += 64 * V * U) {
+            const long long c = c0 + l * V;
+            Pack<T> g[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) g[u] = ld<T>(dout + t * D, c + u * 64 * V, D);
+            for (int j = 0; j < m; ++j) {
+                const int p = __builtin_amdgcn_readlane(pos, j);
+                if (p < 0) continue;
+                const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wt), j));
+                Pack<T> y[U];
+                if (dw)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) y[u] = ld<T>(ys + (long long)p * D, c + u * 64 * V, D);
+                if (dys)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        Pack<T> o;
+#pragma unroll
+                        for (int q = 0; q < V; ++q) o.v[q] = from_f<T>(wj * to_f(g[u].v[q]));
+                        st<T>(dys + (long long)p * D, c + u * 64 * V, D, o);
+                    }
                 if (dw) {
-                    const Pack<T, V> y = ld<T, V>(ys + (long long)p * D + c);
+                    float dot = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) dot = fmaf(to_f(g.v[i]), to_f(y.v[i]), dot);
-                }
-                if (dys) {
-                    Pack<T, V> o;
+                    for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(wj * to_f(g.v[i]));
-                    st<T, V>(dys + (long long)p * D + c, o);
+                        for (int q = 0; q < V; ++q) dot = fmaf(to_f(g[u].v[q]), to_f(y[u].v[q]), dot);
+                    dot = wave_sum_f32(dot);
+                    mine += l == j ? dot : 0.0f;
                 }
             }
-            if (dw) {
-                dot = wave_sum_f32(dot);
-                if (l == j) mine = dot;
-            }
+            if (dys) zero_unused<T, U>(dys, off, E, P, D, t, T_, c);
         }
         if (dw && l < m) dw[t * m + l] = mine;
-        if (dys) zero_unused<T, V>(dys, off, E, P, D, t, T_);
     }
 }
 
-// calls f with an element type and the elements of a 16-byte load when every
-// row starts on 16 bytes, else one element at a time
+// Calls f with an element type and U.  Several stretches a wave where that
+// still leaves enough waves for the chip's 1024 SIMDs, else one: (4 tokens of
+// 4096 x 8 slots in bf16: 17.7 us with a wave a token, 3 us with U = 1;
+// 16384 tokens of 2048 x 4: 101 us with one load in flight, 75 us with U = 4).
 template <class F>
-static void with_pack(int dtype, long long D, std::initializer_list<const void*> ptrs, F&& f) {
-    bool wide = D * (long long)dtype_size(dtype) % 16 == 0;
-    for (const void* p : ptrs) wide = wide && aligned16(p);
+static void with_stretches(int dtype, long long T, long long D, F&& f) {
     with_dtype(dtype, [&](auto v) {
-        using T = decltype(v);
-        if (wide) f(v, std::integral_constant<int, 16 / (int)sizeof(T)>{});
-        else f(v, std::integral_constant<int, 1>{});
+        using S = decltype(v);
+        constexpr int kLanes = 64 * Pack<S>::V;
+        if (T * ceil_div(D, 4 * kLanes) >= 4096) f(v, std::integral_constant<int, 4>{}, (int)ceil_div(D, 4 * kLanes));
+        else f(v, std::integral_constant<int, 1>{}, (int)ceil_div(D, kLanes));
     });
 }
-static dim3 tok_grid(long long T) { return dim3(grid_of(ceil_div(T, kTokWaves))); }
+static dim3 wave_grid(long long waves) { return dim3(grid_of(ceil_div(waves, kTokWaves))); }
 
 void launch_dispatch(const void* x, int dtype, long long T, int m, long long D, int E, const int32_t* offsets,
                      const int32_t* place, void* xs, hipStream_t st) {
     if (T < 1 || D < 1) return;
-    with_pack(dtype, D, {x, xs}, [&](auto tv, auto vv) {
+    with_stretches(dtype, T, D, [&](auto tv, auto uv, int n) {
         using S = decltype(tv);
-        constexpr int V = decltype(vv)::value;
-        hipLaunchKernelGGL((k_dispatch<S, V>), tok_grid(T), dim3(kTokThreads), 0, st, (const S*)x, T, m, D, E, offsets,
-                           place, (S*)xs);
+        constexpr int U = decltype(uv)::value;
+        hipLaunchKernelGGL((k_dispatch<S, U>), wave_grid(T * n), dim3(kTokThreads), 0, st, (const S*)x, T, m, D, E, n,
+                           offsets, place, (S*)xs);
     });
 }
 
@@ -182,21 +255,20 @@ void launch_dispatch_vjp(const void* dxs, int dtype, long long T, int m, long lo
 void launch_combine(const void* ys, const float* w, const void* residual, int dtype, long long T, int m, long long D,
                     const int32_t* place, void* out, hipStream_t st) {
     if (T < 1 || D < 1) return;
-    with_pack(dtype, D, {ys, residual, out}, [&](auto tv, auto vv) {
+    with_stretches(dtype, T, D, [&](auto tv, auto uv, int n) {
         using S = decltype(tv);
-        constexpr int V = decltype(vv)::value;
-        hipLaunchKernelGGL((k_combine<S, V>), tok_grid(T), dim3(kTokThreads), 0, st, (const S*)ys, w,
-                           (const S*)residual, T, m, D, place, (S*)out);
+        constexpr int U = decltype(uv)::value;
+        hipLaunchKernelGGL((k_combine<S, U>), wave_grid(T * n), dim3(kTokThreads), 0, st, (const S*)ys, w,
+                           (const S*)residual, T, m, D, n, place, (S*)out);
     });
 }
 
 void launch_combine_vjp(const void* ys, const float* w, const void* dout, int dtype, long long T, int m, long long D,
                         int E, const int32_t* offsets, const int32_t* place, void* dys, float* dw, hipStream_t st) {
     if (T < 1) return;
-    with_pack(dtype, D, {ys, dout, dys}, [&](auto tv, auto vv) {
+    with_dtype(dtype, [&](auto tv) {
         using S = decltype(tv);
-        constexpr int V = decltype(vv)::value;
-        hipLaunchKernelGGL((k_combine_vjp<S, V>), tok_grid(T), dim3(kTokThreads), 0, st, (const S*)ys, w,
+        hipLaunchKernelGGL((k_combine_vjp<S, 4>), wave_grid(T), dim3(kTokThreads), 0, st, (const S*)ys, w,
                            (const S*)dout, T, m, D, E, offsets, place, (S*)dys, dw);
     });
 }

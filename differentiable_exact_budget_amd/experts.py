@@ -18,12 +18,11 @@ Rows may be float32, bfloat16 or float16; gates and weights are float32.
 Sums are held in float32 and rounded once to the rows' type.
 """
 import ctypes
-from dataclasses import dataclass
 
 import torch
 
+from . import _binding
 from ._binding import LapsumError
-from ._binding import lib as _load
 
 __all__ = ["ExpertPlan", "expert_topk", "expert_topk_vjp", "expert_sort", "expert_dispatch", "expert_dispatch_vjp",
            "expert_linear", "expert_linear_vjp", "expert_combine", "expert_combine_vjp", "ACTIVATIONS",
@@ -43,10 +42,13 @@ _lib = None
 
 
 def lib():
-    """liblapsum.so with the expert operators' argument types set."""
+    """liblapsum.so with the expert operators' argument types set.  These
+    calls only launch, so they keep the interpreter lock (PyDLL): giving it up
+    and taking it again costs more than the call."""
     global _lib
     if _lib is None:
-        L = _load()
+        _binding.lib()  # raises if it is not built
+        L = ctypes.PyDLL(_binding.LIB_PATH)
         vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
         types = {
             "lapsum_expert_topk": [vp, i64, i64, i64, f32, i32, vp, vp, vp, vp],
@@ -93,6 +95,11 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
+def _recorded(*inputs) -> bool:
+    """Whether autograd has to see the call."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
+
+
 def _any_rows(*outputs) -> bool:
     """Whether any output is wanted and has elements to write."""
     return any(t is not None and t.numel() for t in outputs)
@@ -100,13 +107,16 @@ def _any_rows(*outputs) -> bool:
 
 def _run(name: str, device, *args) -> None:
     """Calls the C entry point on the device's current stream."""
-    with torch.cuda.device(device):
-        rc = getattr(lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    f, i = getattr(_lib or lib(), name), device.index
+    if i == torch.cuda.current_device():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
     if rc != 0:
         raise LapsumError(rc, name)
 
 
-@dataclass(frozen=True)
 class ExpertPlan:
     """Where every (token, slot) pair goes, as expert_sort makes it.
 
@@ -114,10 +124,10 @@ class ExpertPlan:
     offsets[experts] is the number of pairs in use; order[pos] is the pair
     token * slots + slot at a position (-1 past the used ones), place[token,
     slot] the position of a pair (-1 for an empty slot).  All int32."""
-    experts: int
-    offsets: torch.Tensor
-    order: torch.Tensor
-    place: torch.Tensor
+    __slots__ = ("experts", "offsets", "order", "place")
+
+    def __init__(self, experts: int, offsets: torch.Tensor, order: torch.Tensor, place: torch.Tensor):
+        self.experts, self.offsets, self.order, self.place = experts, offsets, order, place
 
     @property
     def tokens(self) -> int:
@@ -211,6 +221,8 @@ def expert_topk(p: torch.Tensor, m: int, *, floor: float = float("-inf"), normal
     Differentiable with respect to p through w."""
     if not isinstance(p, torch.Tensor):
         raise TypeError("p must be a torch.Tensor")
+    if not _recorded(p):
+        return _topk(p.contiguous(), int(m), float(floor), bool(normalize))[:2]
     return ExpertTopK.apply(p, int(m), float(floor), bool(normalize))
 
 
@@ -275,6 +287,8 @@ def expert_dispatch(x: torch.Tensor, plan: ExpertPlan) -> torch.Tensor:
     the pair's place, zeros past the used places."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
+    if not _recorded(x):
+        return _dispatch(x.contiguous(), plan)
     return ExpertDispatch.apply(x, plan)
 
 
@@ -358,6 +372,9 @@ def expert_linear(xs: torch.Tensor, weight: torch.Tensor, plan: ExpertPlan, *, b
     "gelu" (the exact one, with the error function)."""
     if not isinstance(xs, torch.Tensor) or not isinstance(weight, torch.Tensor):
         raise TypeError("xs and weight must be torch.Tensors")
+    if not _recorded(xs, weight, bias):
+        return _linear(xs.contiguous(), weight.contiguous(), plan, bias.contiguous() if bias is not None else None,
+                       activation, False)[0]
     return ExpertLinear.apply(xs, weight, bias, plan, activation)
 
 
@@ -420,4 +437,6 @@ def expert_combine(ys: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, *,
     w[token, slot] times the slot's row of ys; empty slots add nothing."""
     if not isinstance(ys, torch.Tensor) or not isinstance(w, torch.Tensor):
         raise TypeError("ys and w must be torch.Tensors")
+    if not _recorded(ys, w, residual):
+        return _combine(ys.contiguous(), w.contiguous(), plan, residual.contiguous() if residual is not None else None)
     return ExpertCombine.apply(ys, w, residual, plan)
