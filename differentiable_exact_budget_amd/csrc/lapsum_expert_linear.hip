@@ -152,6 +152,16 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
 // A workgroup takes kDzRows rows of one expert and 64 V columns, a wave a
 // quarter of the rows; the waves' sums are added in wave order, one partial
 // row per tile of rows, and k_dbias adds an expert's partials in their order.
+template <class R>
+LS_DEV R once(const void* p) {
+    if constexpr (sizeof(R) == 16) {
+        typedef uint32_t Words __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(R, __builtin_nontemporal_load(reinterpret_cast<const Words*>(p)));
+    } else {
+        return *reinterpret_cast<const R*>(p);
+    }
+}
+
 template <class T, int ACT, int V>
 LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const int32_t* __restrict__ off, int P,
                     int E, int N, T* __restrict__ dz, float* __restrict__ part, int ti, int tj, float (*s)[64 * V]) {
@@ -163,8 +173,12 @@ LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const
     float sum[V] = {};
     // four rows' loads are in flight at a time
     constexpr int U = 4;
-    struct __attribute__((aligned(sizeof(T) * V))) PT { T v[V]; };
-    struct __attribute__((aligned(sizeof(Z) * V))) PZ { Z v[V]; };
+    struct __attribute__((aligned(sizeof(T) * V))) PT {
+        T v[V];
+    };
+    struct __attribute__((aligned(sizeof(Z) * V))) PZ {
+        Z v[V];
+    };
     if (c < N) {
         for (int r0 = t.lo + w; r0 < t.hi; r0 += 4 * U) {
             PT g[U];
@@ -172,8 +186,9 @@ LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const long long at = (long long)min(r0 + 4 * u, t.hi - 1) * N + c;
-                g[u] = *reinterpret_cast<const PT*>(dy + at);
-                if (ACT != kActNone) z[u] = *reinterpret_cast<const PZ*>((const Z*)zp + at);
+                // read once: past the caches, which dz is to fill
+                g[u] = once<PT>(dy + at);
+                if (ACT != kActNone) z[u] = once<PZ>((const Z*)zp + at);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {

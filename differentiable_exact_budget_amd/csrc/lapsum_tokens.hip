@@ -34,13 +34,20 @@ template <class T>
 struct __attribute__((packed, aligned(sizeof(T)))) Loose {
     Pack<T> p;
 };
-// elements c .. of a row of D elements; past the row's end: zeros
-template <class T>
+// Elements c .. of a row of D elements; past the row's end: zeros.  ONCE:
+// rows that no later part of the pass reads go past the caches (rows gathered
+// from 255 MB, 16384 tokens x 4 x 2048 bf16: combine 99 -> 70 us, its VJP
+// 129 -> 94 us; dispatch, whose x fits them, is 2 us slower that way).
+template <bool ONCE, class T>
 LS_DEV Pack<T> ld(const T* row, long long c, long long D) {
     constexpr int V = Pack<T>::V;
+    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));  // at any element
     Pack<T> x{};
     if (c + V <= D) {
-        x = reinterpret_cast<const Loose<T>*>(row + c)->p;
+        if (ONCE)
+            x = __builtin_bit_cast(Pack<T>, __builtin_nontemporal_load(reinterpret_cast<const Words*>(row + c)));
+        else
+            x = reinterpret_cast<const Loose<T>*>(row + c)->p;
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -101,7 +108,7 @@ __global__ __launch_bounds__(kTokThreads) void k_dispatch(const T* __restrict__ 
         const long long c = a.c0 + lane_id() * V;
         Pack<T> v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = ld<T>(x + a.t * D, c + u * 64 * V, D);
+        for (int u = 0; u < U; ++u) v[u] = ld<false>(x + a.t * D, c + u * 64 * V, D);
         for (int j = 0; j < m; ++j) {
             const int p = __builtin_amdgcn_readlane(pos, j);
             if (p < 0) continue;
@@ -130,7 +137,7 @@ __global__ __launch_bounds__(kTokThreads) void k_combine(const T* __restrict__ y
         if (residual) {
             Pack<T> v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = ld<T>(residual + a.t * D, c + u * 64 * V, D);
+            for (int u = 0; u < U; ++u) v[u] = ld<true>(residual + a.t * D, c + u * 64 * V, D);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -144,10 +151,10 @@ __global__ __launch_bounds__(kTokThreads) void k_combine(const T* __restrict__ y
             Pack<T> v0[U] = {}, v1[U] = {};
             if (p0 >= 0)
 #pragma unroll
-                for (int u = 0; u < U; ++u) v0[u] = ld<T>(ys + (long long)p0 * D, c + u * 64 * V, D);
+                for (int u = 0; u < U; ++u) v0[u] = ld<true>(ys + (long long)p0 * D, c + u * 64 * V, D);
             if (p1 >= 0)
 #pragma unroll
-                for (int u = 0; u < U; ++u) v1[u] = ld<T>(ys + (long long)p1 * D, c + u * 64 * V, D);
+                for (int u = 0; u < U; ++u) v1[u] = ld<true>(ys + (long long)p1 * D, c + u * 64 * V, D);
             if (p0 >= 0)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -188,7 +195,7 @@ __global__ __launch_bounds__(kTokThreads) void k_combine_vjp(const T* __restrict
             const long long c = c0 + l * V;
             Pack<T> g[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) g[u] = ld<T>(dout + t * D, c + u * 64 * V, D);
+            for (int u = 0; u < U; ++u) g[u] = ld<true>(dout + t * D, c + u * 64 * V, D);
             for (int j = 0; j < m; ++j) {
                 const int p = __builtin_amdgcn_readlane(pos, j);
                 if (p < 0) continue;
@@ -196,7 +203,7 @@ __global__ __launch_bounds__(kTokThreads) void k_combine_vjp(const T* __restrict
                 Pack<T> y[U];
                 if (dw)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) y[u] = ld<T>(ys + (long long)p * D, c + u * 64 * V, D);
+                    for (int u = 0; u < U; ++u) y[u] = ld<true>(ys + (long long)p * D, c + u * 64 * V, D);
                 if (dys)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
@@ -224,7 +231,7 @@ __global__ __launch_bounds__(kTokThreads) void k_combine_vjp(const T* __restrict
 // Calls f with an element type and U.  Several stretches a wave where that
 // still leaves enough waves for the chip's 1024 SIMDs, else one: (4 tokens of
 // 4096 x 8 slots in bf16: 17.7 us with a wave a token, 3 us with U = 1;
-// 16384 tokens of 2048 x 4: 101 us with one load in flight, 75 us with U = 4).
+// 65536 x 4 rows at U = 1 and 4 within 2%).
 template <class F>
 static void with_stretches(int dtype, long long T, long long D, F&& f) {
     with_dtype(dtype, [&](auto v) {
