@@ -15,7 +15,8 @@ OUT = os.path.join(HERE, "liblapsum.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["lapsum_sample.hip", "lapsum_stream.hip", "lapsum_sort.hip", "lapsum_ceiling.hip", "lapsum_topk.hip", "lapsum_batched.hip", "lapsum_heavy.hip", "lapsum_noalloc.hip", "lapsum_route.hip", "lapsum_tokens.hip",
-           "lapsum_expert_linear.hip", "lapsum_expert_mfma.hip", "lapsum_host.cpp", "lapsum_experts_host.cpp"]
+           "lapsum_expert_linear.hip", "lapsum_expert_mfma.hip", "lapsum_expert_few.hip",
+           "lapsum_host.cpp", "lapsum_experts_host.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang",

@@ -1,124 +1,219 @@
-// The experts' products: every expert's weights against its own rows, forward
-// and both gradients, in matrix instructions.
+// The experts' products for every type, size and alignment, and dz with the
+// bias gradient.
 //
-// k_product_any takes every type, size and alignment: a workgroup forms a
-// 64 x 64 tile of one expert's result, staging 32 steps of the sum at a time
-// in LDS as fp32 and multiplying with the fp32 matrix instruction
-// (v_mfma_f32_32x32x2_f32), so 16-bit rows lose nothing on the way.
-#include "lapsum_expert_ops.h"
+// k_product_any takes what the 16-bit tile kernels do not: fp32 rows, and
+// 16-bit rows whose widths or addresses are off 16 bytes.  Operands go from
+// memory through registers to LDS, 16 bytes a lane at any element's address
+// (the hardware takes those), only the ends of rows element by element.  16-bit
+// rows are multiplied by the 16-bit matrix instruction, fp32 rows by the fp32
+// one (v_mfma_f32_32x32x2_f32), which bounds them.
+//  - Many tiles: 128 x 128 a workgroup, 64 x 64 a wave; two LDS buffers of two
+//    steps each, the next two steps' loads in flight while two are multiplied.
+//  - Few tiles: 32 x 32 a workgroup, and its four waves split the sum, each on
+//    its own in its own part of LDS; their results are added in wave order.
+#include "lapsum_expert_tile.h"
 
 namespace lapsum {
 
-constexpr int kAnyTile = 64;
-constexpr int kAnyK = 32;
 constexpr int kAnyThreads = 256;
-constexpr int kAnyPad = kAnyTile + 4;
+constexpr int kAnySteps = 2;  // steps of 64 bytes of k in a buffer
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+// One operand: R rows by one step of k, dealt out to NT threads in chunks.
+template <class T, int R, bool KFAST, bool PAIRED, int NT>
+struct AnyOperand : StepLds<R, KFAST, PAIRED> {
+    using Lds = StepLds<R, KFAST, PAIRED>;
+    static constexpr int kPer = 16 / (int)sizeof(T);      // elements of a chunk
+    static constexpr int kStepK = 64 / (int)sizeof(T);    // k of a step
+    static constexpr int kLoads = R * 64 / (NT * 16);     // a thread's chunks per step
+    static constexpr int kRow = KFAST ? 4 : R / kPer;     // chunks of a row of memory
 
-// One tile of the operand X(i, k), i < n, k < K, into s[k][i]; zeros outside.
-// KFAST: k is the contiguous index (X[i * ld + k]), else i (X[k * ld + i]).
-template <class T, bool KFAST>
-struct AnyLoad {
-    static constexpr int kN = kAnyTile * kAnyK / kAnyThreads;
-    float r[kN];
-    LS_DEV void get(const T* __restrict__ x, long long ld, long long i0, long long n, long long k0, long long K) {
+    // chunks of k0 .. of X (row i, k: x[i * ld + k], or x[k * ld + i]), zeros
+    // past `own` rows and K
+    static LS_DEV void get(u32x4 (&r)[kLoads], const T* __restrict__ x, long long ld, int own, int k0, int K, int tid) {
 #pragma unroll
-        for (int q = 0; q < kN; ++q) {
-            const int at = q * kAnyThreads + threadIdx.x;
-            const long long i = i0 + (KFAST ? at / kAnyK : at % kAnyTile);
-            const long long k = k0 + (KFAST ? at % kAnyK : at / kAnyTile);
-            r[q] = i < n && k < K ? to_f(x[KFAST ? i * ld + k : k * ld + i]) : 0.0f;
+        for (int i = 0; i < kLoads; ++i) {
+            const int q = i * NT + tid, line = q / kRow, at = q % kRow * kPer;
+            const int row = KFAST ? line : k0 + line, col = KFAST ? k0 + at : at;
+            const int left = row < (KFAST ? own : K) ? (KFAST ? K : own) - col : 0;
+            const T* p = x + row * ld + col;
+            typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));  // at any element
+            if (left >= kPer) {
+                r[i] = *reinterpret_cast<const Words*>(p);
+            } else {
+                struct { T v[kPer]; } e = {};
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (j < left) e.v[j] = p[j];
+                r[i] = __builtin_bit_cast(u32x4, e);
+            }
         }
     }
-    LS_DEV void put(float (*s)[kAnyPad]) const {
+    static LS_DEV void put(const u32x4 (&r)[kLoads], char* lds, int tid) {
 #pragma unroll
-        for (int q = 0; q < kN; ++q) {
-            const int at = q * kAnyThreads + threadIdx.x;
-            s[KFAST ? at % kAnyK : at / kAnyTile][KFAST ? at / kAnyK : at % kAnyTile] = r[q];
+        for (int i = 0; i < kLoads; ++i) {
+            const int q = i * NT + tid, line = q / kRow, c = q % kRow;
+            int at;
+            if (KFAST) at = (line >> 1) * 128 + (((line & 1) * 4 + c) ^ Lds::fold(line >> 1 & 7)) * 16;
+            else at = line * (R * (int)sizeof(T)) + (sizeof(T) == 2 ? c ^ Lds::fold(line) : c) * 16;
+            *(u32x4*)(lds + at) = r[i];
         }
     }
 };
 
-// tile `ti` of the rows (or of expert and output), `tj` of the columns
+// One row's element (i, j) of a piece from its sum
 template <class T, int FORM, int ACT>
-LS_DEV void product_any(const LinearArgs& g, int ti, int tj, float (*sa)[kAnyPad], float (*sb)[kAnyPad]) {
-    using Z = typename ZKeep<T>::type;
-    // this workgroup's part of the result: rows i0.. of M (from C row c0),
-    // columns j0.. of N; the sum runs over K
-    const long long j0 = (long long)tj * kAnyTile;
-    long long M, N, K, i0, lda, ldb;
-    const T *a = (const T*)g.a, *b = (const T*)g.b;
-    T* c = (T*)g.c;
-    const T* bias = nullptr;
-    Z* z = nullptr;
-    if (FORM == kFormDw) {
-        const int to = (g.out + kAnyTile - 1) / kAnyTile;
-        const int e = ti / to;
-        const int lo = row_at(g.off, e, g.P), hi = max(row_at(g.off, e + 1, g.P), lo);
-        i0 = (long long)(ti % to) * kAnyTile;
-        M = g.out, N = g.in, K = hi - lo, lda = g.out, ldb = g.in;
-        a += lo * lda;
-        b += lo * ldb;
-        c += (long long)e * g.out * g.in;
+LS_DEV void put_any(const Piece<T>& p, long long i, int j, float v) {
+    if (FORM == kFormY && p.bias) v += to_f(p.bias[j]);
+    if (FORM == kFormY && ACT != kActNone && p.z) p.z[i * p.ldc + j] = ZKeep<T>::template make<ACT>(v);
+    p.c[i * p.ldc + j] = from_f<T>(act_of<ACT, T>(v));
+}
+
+// B x B of a piece from row i0 and column j0; SPLIT: the waves share the sum
+template <class T, int FORM, int ACT, int B, bool SPLIT>
+LS_DEV void any_tile(const Piece<T>& p, int i0, int j0, char* lds) {
+    constexpr bool kA = FORM != kFormDw, kB = FORM == kFormY;
+    constexpr bool k16 = sizeof(T) == 2;
+    constexpr int NT = SPLIT ? 64 : kAnyThreads;
+    using OpA = AnyOperand<T, B, kA, false, NT>;
+    using OpB = AnyOperand<T, B, kB, k16, NT>;
+    constexpr int kStepK = OpA::kStepK, kDeep = kAnySteps * kStepK;
+    constexpr int kBuffer = kAnySteps * (OpA::kBytes + OpB::kBytes);
+    constexpr int W = SPLIT ? B : B / 2;         // a wave's rows and columns
+    constexpr int FR = k16 ? 16 : 32, F = W / FR;  // fragments
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+    const int r0 = SPLIT ? 0 : (w >> 1) * W, c0 = SPLIT ? 0 : (w & 1) * W;
+    const int tid = SPLIT ? l : (int)threadIdx.x;
+    const T* a = p.a + (kA ? (long long)i0 * p.lda : i0);
+    const T* b = p.b + (kB ? (long long)j0 * p.ldb : j0);
+    const int M = p.M - i0, N = p.N - j0;
+    int k0 = 0, K = p.K;
+    if (SPLIT) {  // this wave's share of the sum, in whole buffers
+        const int deep = (K + kDeep - 1) / kDeep;
+        k0 = w * deep / 4 * kDeep;
+        K = min(K, (w + 1) * deep / 4 * kDeep);
+        lds += w * 2 * kBuffer;
+    }
+    using Acc = std::conditional_t<k16, f32x4, f32x16>;
+    Acc acc[F][F] = {};
+    u32x4 ra[kAnySteps][OpA::kLoads], rb[kAnySteps][OpB::kLoads];
+    auto get = [&](int k) {
+#pragma unroll
+        for (int h = 0; h < kAnySteps; ++h) {
+            OpA::get(ra[h], a, p.lda, M, k + h * kStepK, K, tid);
+            OpB::get(rb[h], b, p.ldb, N, k + h * kStepK, K, tid);
+        }
+    };
+    if (k0 < K) get(k0);
+    int buf = 0;
+    for (; k0 < K; k0 += kDeep) {
+        char* s = lds + buf;
+#pragma unroll
+        for (int h = 0; h < kAnySteps; ++h) {
+            OpA::put(ra[h], s + h * OpA::kBytes, tid);
+            OpB::put(rb[h], s + kAnySteps * OpA::kBytes + h * OpB::kBytes, tid);
+        }
+        // (a wave's own LDS operations are served in order)
+        if (SPLIT) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        else __syncthreads();
+        if (k0 + kDeep < K) get(k0 + kDeep);
+#pragma unroll
+        for (int h = 0; h < kAnySteps; ++h) {
+            const char *sa = s + h * OpA::kBytes, *sb = s + kAnySteps * OpA::kBytes + h * OpB::kBytes;
+            if constexpr (k16) {
+                s16x8 fa[F], fb[F];
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    fb[i] = OpB::frag(sb, c0, i);
+                    fa[i] = OpA::frag(sa, r0, i);
+                }
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+#pragma unroll
+                    for (int j = 0; j < F; ++j) acc[i][j] = mfma16<T>(fb[j], fa[i], acc[i][j]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    f32x4 fa[F], fb[F];
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        fa[i] = OpA::frag32(sa, r0, i, q);
+                        fb[i] = OpB::frag32(sb, c0, i, q);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int i = 0; i < F; ++i)
+#pragma unroll
+                            for (int j = 0; j < F; ++j)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i][e], fb[j][e], acc[i][j], 0, 0, 0);
+                }
+            }
+        }
+        buf = kBuffer - buf;
+    }
+    // where a lane's sums lie: 16-bit, row l % 16 of fragment i and columns
+    // 8 (l / 16) + 4 (j & 1) + r of the pair j / 2; fp32, rows
+    // 8 (r / 4) + 4 (l / 32) + r % 4 and column l % 32
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j)
+#pragma unroll
+                for (int r = 0; r < (k16 ? 4 : 16); ++r) {
+                    if constexpr (k16)
+                        f(r0 + i * 16 + (l & 15), c0 + (j >> 1) * 32 + (l >> 4) * 8 + (j & 1) * 4 + r, acc[i][j][r]);
+                    else
+                        f(r0 + i * 32 + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), c0 + j * 32 + (l & 31), acc[i][j][r]);
+                }
+    };
+    if constexpr (SPLIT) {
+        __syncthreads();
+        constexpr int kPad = B + 1;
+        float* part = reinterpret_cast<float*>(lds - w * 2 * kBuffer);
+        each([&](int i, int j, float v) { part[(w * B + i) * kPad + j] = v; });
+        __syncthreads();
+        for (int q = threadIdx.x; q < B * B; q += kAnyThreads) {
+            const int i = q / B, j = q % B;
+            float v = part[i * kPad + j];
+#pragma unroll
+            for (int o = 1; o < 4; ++o) v += part[(o * B + i) * kPad + j];
+            if (i < M && j < N) put_any<T, FORM, ACT>(p, i0 + i, j0 + j, v);
+        }
     } else {
-        const RowTile t = find_row_tile<kAnyTile>(g.off, g.E, g.P, ti);
-        if (t.lo >= t.hi) return;
-        const bool unused = t.e >= g.E;
-        i0 = 0, M = t.hi - t.lo;
-        K = FORM == kFormY ? g.in : g.out;
-        N = FORM == kFormY ? g.out : g.in;
-        lda = K, ldb = g.in;
-        a += t.lo * lda;
-        c += t.lo * N;
-        if (unused) {
-            K = 0;
-        } else {
-            b += (long long)t.e * g.out * g.in;
-            if (FORM == kFormY && g.bias) bias = (const T*)g.bias + (long long)t.e * g.out;
-            if (FORM == kFormY && g.z) z = (Z*)g.z + t.lo * N;
-        }
-    }
-    const int l = lane_id(), w = threadIdx.x >> 6;
-    const int wi = (w >> 1) * 32, wj = (w & 1) * 32;
-    f32x16 acc = {};
-    AnyLoad<T, FORM != kFormDw> la;
-    AnyLoad<T, FORM == kFormY> lb;
-    la.get(a, lda, i0, M, 0, K);
-    lb.get(b, ldb, j0, N, 0, K);
-    for (long long k0 = 0; k0 < K; k0 += kAnyK) {
-        la.put(sa);
-        lb.put(sb);
-        __syncthreads();
-        if (k0 + kAnyK < K) {
-            la.get(a, lda, i0, M, k0 + kAnyK, K);
-            lb.get(b, ldb, j0, N, k0 + kAnyK, K);
-        }
-#pragma unroll
-        for (int k = 0; k < kAnyK; k += 2)
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sa[k + (l >> 5)][wi + (l & 31)],
-                                                       sb[k + (l >> 5)][wj + (l & 31)], acc, 0, 0, 0);
-        __syncthreads();
-    }
-    // lane l holds column l % 32, rows 8 (r / 4) + 4 (l / 32) + r % 4
-    const long long j = j0 + wj + (l & 31);
-    if (j >= N) return;
-    const float bj = bias ? to_f(bias[j]) : 0.0f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const long long i = i0 + wi + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3);
-        if (i >= M) continue;
-        const float v = acc[r] + bj;
-        if (z) z[i * N + j] = ZKeep<T>::template make<ACT>(v);
-        c[i * N + j] = from_f<T>(act_of<ACT, T>(v));
+        each([&](int i, int j, float v) {
+            if (i < M && j < N) put_any<T, FORM, ACT>(p, i0 + i, j0 + j, v);
+        });
     }
 }
 
-template <class T, int FORM, int ACT>
+template <class T, int FORM, int ACT, int B, bool SPLIT>
 __global__ __launch_bounds__(kAnyThreads) void k_product_any(LinearArgs g, long long tiles, int cols) {
-    __shared__ float sa[kAnyK][kAnyPad], sb[kAnyK][kAnyPad];
-    for (long long t = blockIdx.x; t < tiles; t += gridDim.x)
-        product_any<T, FORM, ACT>(g, (int)(t / cols), (int)(t % cols), sa, sb);
+    __shared__ __align__(128) char lds[2 * kAnySteps * 2 * B * 64 * (SPLIT ? 4 : 1)];
+    for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+        // tiles past the last (their number is only bounded here) have no rows
+        const Place<T> at = find_place<T, FORM, B>(g, (int)t, cols);
+        if (at.rows > 0 && at.q < at.rows * cols)
+            any_tile<T, FORM, ACT, B, SPLIT>(at.p, at.q / cols * B, at.q % cols * B, lds);
+        __syncthreads();
+    }
+}
+
+template <class T, int B, bool SPLIT>
+static void launch_any(int form, const LinearArgs& g, hipStream_t st) {
+    const int N = form == kFormY ? g.out : g.in;
+    const long long cols = ceil_div(N, B);
+    const long long tiles = cols * (form == kFormDw ? ceil_div(g.out, B) * g.E : max_row_tiles<B>(g.P, g.E));
+    const dim3 grid(grid_of(tiles)), block(kAnyThreads);
+    if (form == kFormDw)
+        hipLaunchKernelGGL((k_product_any<T, kFormDw, kActNone, B, SPLIT>), grid, block, 0, st, g, tiles, (int)cols);
+    else if (form == kFormDx)
+        hipLaunchKernelGGL((k_product_any<T, kFormDx, kActNone, B, SPLIT>), grid, block, 0, st, g, tiles, (int)cols);
+    else
+        with_act(g.act, [&](auto av) {
+            hipLaunchKernelGGL((k_product_any<T, kFormY, decltype(av)::value, B, SPLIT>), grid, block, 0, st, g, tiles,
+                               (int)cols);
+        });
 }
 
 void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t st) {
@@ -128,21 +223,12 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
         launch_expert_mfma(form, dtype, g, st);
         return;
     }
-    const long long cols = ceil_div(N, kAnyTile);
-    const long long tiles =
-        cols * (form == kFormDw ? ceil_div(g.out, kAnyTile) * g.E : max_row_tiles<kAnyTile>(g.P, g.E));
-    const dim3 grid(grid_of(tiles)), block(kAnyThreads);
+    // 128 x 128 tiles where they fill the CUs
+    const long long tiles = ceil_div(N, 128) * (form == kFormDw ? ceil_div(g.out, 128) * g.E : g.P / 128 + g.E / 2);
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
-        if (form == kFormDw)
-            hipLaunchKernelGGL((k_product_any<T, kFormDw, kActNone>), grid, block, 0, st, g, tiles, (int)cols);
-        else if (form == kFormDx)
-            hipLaunchKernelGGL((k_product_any<T, kFormDx, kActNone>), grid, block, 0, st, g, tiles, (int)cols);
-        else
-            with_act(g.act, [&](auto av) {
-                hipLaunchKernelGGL((k_product_any<T, kFormY, decltype(av)::value>), grid, block, 0, st, g, tiles,
-                                   (int)cols);
-            });
+        if (tiles >= 192) launch_any<T, 128, false>(form, g, st);
+        else launch_any<T, 32, true>(form, g, st);
     });
 }
 

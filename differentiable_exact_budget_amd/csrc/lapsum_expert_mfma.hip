@@ -23,43 +23,18 @@
 //  - Reads out of range return zero, which is all the masking that ragged
 //    experts need: a tile's buffer ends with its expert's last row.
 //
-// LDS layout of a step, free of bank conflicts for the fragment reads below:
-//   k contiguous: row i has 32 k = 4 chunks of 16 bytes, two rows to a line
-//     of 128; chunk c lies at c ^ fold(line) within its row's half.  A
-//     fragment is one 16-byte read a lane.
-//   own index contiguous: row k has BM (BN) elements; chunk c lies at
-//     c ^ fold(k).  A fragment is two transposing 8-byte reads
-//     (ds_read_b64_tr_b16).
-// A wave's direct-to-LDS store is 64 consecutive chunks, so the permutation
-// is made on the global side: each lane fetches the chunk that belongs at its
-// place.  B's fragments come in pairs that share 32 columns such that a lane
-// ends with 8 consecutive columns of a row of C, one 16-byte store.
-#include "lapsum_expert_ops.h"
+// A wave's direct-to-LDS store is 64 consecutive chunks of the step's layout
+// in LDS, so the layout's permutation is made on the global side: each lane
+// fetches the chunk that belongs at its place.  B's fragments come in pairs
+// that share 32 columns, so a lane ends with 8 consecutive columns of a row of
+// C, one 16-byte store.
+#include "lapsum_expert_tile.h"
 
 namespace lapsum {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-#define LS_LDS(T) __attribute__((address_space(3))) T
 
 constexpr int kStepK = 32;  // k of one LDS buffer
 constexpr int kRing = 5;    // LDS buffers
 constexpr int kProductThreads = 256;
-
-template <class T>
-LS_DEV f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
-    if constexpr (std::is_same_v<T, __bf16>)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                       0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
-                                                      0, 0);
-}
 
 // 16 bytes a lane from buffer offset `off` to LDS, lane l at `lds` + 16 l.
 // Written as an instruction so that the compiler's counters do not wait for
@@ -84,12 +59,11 @@ LS_DEV void step_barrier() {
 }
 
 // One operand of a tile: R rows (of its own index) by kStepK of k.
-// KFAST: k is contiguous in memory.  PAIRED: fragments 2 j and 2 j + 1 share
-// the rows 32 j .. + 31, row 8 q + 4 (f & 1) + r being row 4 q + r of fragment
-// f; else fragment f has the rows 16 f .. + 15.
 template <int R, bool KFAST, bool PAIRED>
-struct Operand {
-    static constexpr int kBytes = R * kStepK * 2;
+struct Operand : StepLds<R, KFAST, PAIRED> {
+    using Lds = StepLds<R, KFAST, PAIRED>;
+    using Lds::fold;
+    using Lds::kBytes;
     static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads per step
     static constexpr int kChunks = R / 8;                           // chunks of a k row (not KFAST)
 
@@ -100,10 +74,6 @@ struct Operand {
     uint32_t kcol;          // KFAST: first k of this lane's chunk
     uint32_t voff[kLoads];  // this lane's offsets
 
-    static LS_DEV int fold(int q) {
-        if (KFAST) return PAIRED ? (q & 1) | (q >> 1 & 2) : q & 3;
-        return (q & 3) << (PAIRED ? 2 : 1);
-    }
     // x: element (0, 0) of the tile; own: rows left of its own index; K:
     // length of the sum; ld_: elements between memory rows
     template <class T>
@@ -143,36 +113,6 @@ struct Operand {
         const uint32_t off = KFAST && k0 + (int)kcol >= K ? 0x80000000u : voff[i];
         load_to_lds(win, off, lds + (w * kLoads + i) * 1024);
     }
-    // fragment f of the rows from r0: lane l has row l % 16 of it, k 8 (l / 16) .. + 7
-    static LS_DEV s16x8 frag(const char* lds, int r0, int f) {
-        const int l = lane_id(), g = l >> 4, i = l & 15;
-        if (KFAST) {
-            const int r = PAIRED ? (f >> 1) * 32 + (i >> 2) * 8 + (f & 1) * 4 + (i & 3) : f * 16 + i;
-            const int u = ((i & 1) * 4 + g) ^ fold(r >> 1 & 7);
-            return *(const s16x8*)(lds + ((r0 + r) >> 1) * 128 + u * 16);
-        }
-        // the read gives lane l column l % 16 of 16, taken 4 columns at a time
-        // from the places that lanes 4 q + b name: row q, block b
-        // (r0 is a multiple of 64, so the fold changes nothing above a
-        // fragment's own bits, and four addresses serve all fragments)
-        const int k = g * 8 + (i >> 2), b = i & 3;
-        const int c = PAIRED ? ((r0 >> 3) + b) ^ fold(k) ^ (f >> 1) << 2
-                             : (r0 >> 3) + ((f & 3) * 2 + (b >> 1) ^ fold(k)) + (f >> 2) * 8;
-        const char* p = lds + k * (R * 2) + c * 16 + (PAIRED ? f & 1 : b & 1) * 8;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LS_LDS(s16x4)*)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LS_LDS(s16x4)*)(p + 4 * R * 2));
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-};
-
-// What a tile is cut from: A's and B's element (0, 0), C's row 0, the rows
-// and columns left, and the length of the sum.
-template <class T>
-struct Piece {
-    const T *a, *b, *bias;
-    T* c;
-    typename ZKeep<T>::type* z;
-    int M, N, K, lda, ldb, ldc;
 };
 
 // BM x BN of a piece, from its row i0 and column j0
@@ -328,47 +268,13 @@ __global__ __launch_bounds__(kProductThreads) void k_product(LinearArgs g) {
     constexpr int kGroup = 4;  // row tiles that walk the columns together: 4 x 8 tiles on an XCD at a time
     constexpr bool kCut = BM == 256;
     __shared__ __align__(1024) char lds[kRing * (BM + BN) * kStepK * 2];
-    Piece<T> p;
-    p.N = FORM == kFormY ? g.out : g.in;
-    p.ldc = p.N;
-    p.bias = nullptr;
-    p.z = nullptr;
-    const int cols = (p.N + BN - 1) / BN;
-    int q, rows, quarter;  // tile of the expert, its row tiles
-    if (FORM == kFormDw) {
-        rows = (g.out + BM - 1) / BM;
-        const Turn t = take_turn(blockIdx.x, rows * cols * g.E, kCut);
-        if (t.tile < 0) return;
-        const int e = t.tile / (rows * cols);
-        q = t.tile % (rows * cols);
-        quarter = t.quarter;
-        const int lo = uniform(row_at(g.off, e, g.P));
-        p.K = max(uniform(row_at(g.off, e + 1, g.P)) - lo, 0);
-        p.M = g.out, p.lda = g.out, p.ldb = g.in;
-        p.a = (const T*)g.a + (long long)lo * g.out;
-        p.b = (const T*)g.b + (long long)lo * g.in;
-        p.c = (T*)g.c + (long long)e * g.out * g.in;
-    } else {
-        const Turn t = take_turn(blockIdx.x, count_row_tiles<BM>(g.off, g.E, g.P) * cols, kCut);
-        if (t.tile < 0) return;
-        const RowTile at = find_row_tile<BM>(g.off, g.E, g.P, t.tile / cols);
-        const int lo = uniform(row_at(g.off, at.e, g.P));
-        const int hi = at.e < g.E ? max(uniform(row_at(g.off, at.e + 1, g.P)), lo) : g.P;
-        p.M = hi - lo;
-        rows = (p.M + BM - 1) / BM;
-        q = t.tile - at.first * cols;
-        quarter = t.quarter;
-        p.K = at.e == g.E ? 0 : FORM == kFormY ? g.in : g.out;  // unused rows: zeros
-        p.lda = FORM == kFormY ? g.in : g.out;
-        p.ldb = g.in;
-        p.a = (const T*)g.a + (long long)lo * p.lda;
-        p.b = (const T*)g.b + (long long)(at.e < g.E ? at.e : 0) * g.out * g.in;
-        p.c = (T*)g.c + (long long)lo * p.N;
-        if (FORM == kFormY && at.e < g.E) {
-            if (g.bias) p.bias = (const T*)g.bias + (long long)at.e * g.out;
-            if (g.z) p.z = (typename ZKeep<T>::type*)g.z + (long long)lo * p.N;
-        }
-    }
+    const int cols = ((FORM == kFormY ? g.out : g.in) + BN - 1) / BN;
+    const int tiles = FORM == kFormDw ? (g.out + BM - 1) / BM * g.E : count_row_tiles<BM>(g.off, g.E, g.P);
+    const Turn t = take_turn(blockIdx.x, tiles * cols, kCut);
+    if (t.tile < 0) return;
+    const Place<T> at = find_place<T, FORM, BM>(g, t.tile, cols);
+    const Piece<T>& p = at.p;
+    const int q = at.q, rows = at.rows, quarter = t.quarter;
     const int first = q / (kGroup * cols) * kGroup, n = min(kGroup, rows - first);
     const int in = q - first * cols;
     int i0 = (first + in % n) * BM, j0 = in / n * BN;
@@ -383,36 +289,71 @@ __global__ __launch_bounds__(kProductThreads) void k_product(LinearArgs g) {
     form_tile<T, FORM, ACT, BM, BN>(p, i0, j0, lds);
 }
 
-template <class T, int BM, int BN>
+template <class T, int B>
 static void launch_tiles(int form, const LinearArgs& g, hipStream_t st) {
     const int N = form == kFormY ? g.out : g.in;
-    const long long cols = ceil_div(N, BN);
-    const long long tiles = cols * (form == kFormDw ? ceil_div(g.out, BM) * g.E : max_row_tiles<BM>(g.P, g.E));
-    const dim3 grid((unsigned)turns(tiles, BM == 256)), block(kProductThreads);
+    const long long cols = ceil_div(N, B);
+    const long long tiles = cols * (form == kFormDw ? ceil_div(g.out, B) * g.E : max_row_tiles<B>(g.P, g.E));
+    const dim3 grid((unsigned)turns(tiles, B == 256)), block(kProductThreads);
     if (form == kFormDw)
-        hipLaunchKernelGGL((k_product<T, kFormDw, kActNone, BM, BN>), grid, block, 0, st, g);
+        hipLaunchKernelGGL((k_product<T, kFormDw, kActNone, B, B>), grid, block, 0, st, g);
     else if (form == kFormDx)
-        hipLaunchKernelGGL((k_product<T, kFormDx, kActNone, BM, BN>), grid, block, 0, st, g);
+        hipLaunchKernelGGL((k_product<T, kFormDx, kActNone, B, B>), grid, block, 0, st, g);
     else
         with_act(g.act, [&](auto av) {
-            hipLaunchKernelGGL((k_product<T, kFormY, decltype(av)::value, BM, BN>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((k_product<T, kFormY, decltype(av)::value, B, B>), grid, block, 0, st, g);
         });
 }
 
 bool expert_mfma_takes(int form, int dtype, const LinearArgs& g) {
     if (dtype == kF32 || g.in % 8 || g.out % 8 || g.in > (1 << 20) || g.out > (1 << 20)) return false;
     if (!aligned16(g.a) || !aligned16(g.b) || !aligned16(g.c) || !aligned16(g.bias) || !aligned16(g.z)) return false;
-    // tiles counted in 32 bits
-    const long long tiles = form == kFormDw ? ceil_div(g.out, 128) * ceil_div(g.in, 128) * g.E
-                                            : ceil_div(form == kFormY ? g.out : g.in, 128) *
-                                                  max_row_tiles<128>(g.P, g.E);
+    // one tile a workgroup, whatever its side
+    const long long tiles = form == kFormDw ? ceil_div(g.out, 64) * ceil_div(g.in, 64) * g.E
+                                            : ceil_div(form == kFormY ? g.out : g.in, 64) *
+                                                  max_row_tiles<64>(g.P, g.E);
     return tiles < kGridMax;
 }
 
+// The tile's side, by what was measured (bf16, 64 / 128 / 256, us; R: rows of
+// an expert on average; tiles: of 256, the row forms' taken as half filled at
+// each expert's end):
+//   y, 64 experts 2048 -> 1024, R = 1:      30 / 32 / 48    (few rows: more
+//                               R = 16:     45 / 46 / 53    workgroups stream
+//                               R = 64:     85 / 64 / 68    the weights)
+//   y, 8 experts 2048 -> 2048, 160 tiles:   69 / 55 / 58
+//                              288 tiles:  124 / 84 / 81
+//   y, 64 experts 512 -> 1024, 384 tiles:   47 / 37 / 49    (a short sum)
+//   dx, 8 experts 2048 -> 1024, 32 tiles:   20 / 23 / 29
+//   dW, 8 experts, 512 x 512, 32 tiles:     17 / 21 / 21
+//       8 experts, 2048 x 1024, 256 tiles:  21 / 19 / 18
+//       64 experts, 1024 x 2048, R = 1:     79 / 65 / 73
+static int tile_side(int form, const LinearArgs& g) {
+    const long long per = g.P / g.E;
+    if (form == kFormDw) {
+        if (per > 16 && ceil_div(g.out, 256) * ceil_div(g.in, 256) * g.E >= 256) return 256;
+        return ceil_div(g.out, 128) * ceil_div(g.in, 128) * g.E >= 256 ? 128 : 64;
+    }
+    const int N = form == kFormY ? g.out : g.in, K = form == kFormY ? g.in : g.out;
+    if (per >= 96 && K >= 1024 && (g.P / 256 + g.E / 2) * ceil_div(N, 256) >= 256) return 256;
+    return per > 32 && (g.P / 128 + g.E / 2) * ceil_div(N, 128) >= 128 ? 128 : 64;
+}
+
 void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st) {
+    // so few rows that even 64-wide tiles leave most CUs without work: one
+    // token's two experts, 2048 -> 4096: 15 us, 18 us in tiles
+    if (form == kFormY && g.P * ceil_div(g.out, 64) < 256) {
+        launch_expert_few(dtype, g, st);
+        return;
+    }
+    const int side = tile_side(form, g);
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
-        if constexpr (sizeof(T) == 2) launch_tiles<T, 256, 256>(form, g, st);
+        if constexpr (sizeof(T) == 2) {
+            if (side == 256) launch_tiles<T, 256>(form, g, st);
+            else if (side == 128) launch_tiles<T, 128>(form, g, st);
+            else launch_tiles<T, 64>(form, g, st);
+        }
     });
 }
 

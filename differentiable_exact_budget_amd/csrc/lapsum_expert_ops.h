@@ -85,6 +85,8 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
 // lapsum_expert_mfma.hip: the products that the 16-bit matrix instructions take
 bool expert_mfma_takes(int form, int dtype, const LinearArgs& g);
 void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st);
+// lapsum_expert_few.hip: kFormY with few rows an expert, for what expert_mfma_takes
+void launch_expert_few(int dtype, const LinearArgs& g, hipStream_t st);
 // dz (may be null: dz = dy, not written) and per-chunk column sums (may be
 // null) of dz; then the sums per expert
 void launch_expert_dz(const void* z, const void* dy, int dtype, int act, const int32_t* off, int P, int E, int out,

@@ -114,10 +114,8 @@ def linear(xs, weight, bias, offsets, a, dys=None):
     E, F, _ = weight.shape
     o = offsets.tolist()
     x, wt = xs.double(), weight.double()
-    ys, ye = torch.zeros(P, F).double(), torch.zeros(P, F).double()
-    dx, dxe = torch.zeros(P, K).double(), torch.zeros(P, K).double()
-    dw, dwe = torch.zeros(E, F, K).double(), torch.zeros(E, F, K).double()
-    db, dbe = torch.zeros(E, F).double(), torch.zeros(E, F).double()
+    (ys, ye), (dx, dxe), (dw, dwe), (db, dbe) = [[x.new_zeros(s) for _ in range(2)] for s in
+                                                 ((P, F), (P, K), (E, F, K), (E, F))]
     for e in range(E):
         r = slice(o[e], o[e + 1])
         n = o[e + 1] - o[e]
@@ -158,7 +156,7 @@ def linear(xs, weight, bias, offsets, a, dys=None):
 
 
 def check(got, ref, tol, label):
-    got = got.detach().cpu().double()
+    got, ref, tol = got.detach().cpu().double(), ref.cpu(), tol.cpu()
     assert got.shape == ref.shape, f"{label}: shape {tuple(got.shape)}"
     if got.numel() == 0:
         return

@@ -237,14 +237,14 @@ def product_case(dtype, T, m, E, K, F, act, bias=True, drop=0.1, idle=(), seed=0
     return plan, o, xs, weight, b if bias else None, dys, used
 
 
-def check_product(dtype, T, m, E, K, F, act, bias=True, **kw):
+def check_product(dtype, T, m, E, K, F, act, bias=True, on="cpu", **kw):
     plan, o, xs, weight, b, dys, used = product_case(dtype, T, m, E, K, F, act, bias, **kw)
     leaves = [t.cuda().requires_grad_(True) for t in (xs, weight, b) if t is not None]
     y = L.expert_linear(leaves[0], leaves[1], plan, bias=leaves[2] if bias else None, activation=act)
     xs0, dys0, w0 = xs.clone(), dys.clone(), weight.clone()
     xs0[used:] = 0
     dys0[used:] = 0
-    ref = R.linear(xs0, w0, b, o, act, dys0)
+    ref = R.linear(*(None if t is None else t.to(on) for t in (xs0, w0, b)), o, act, dys0.to(on))
     R.check(y, *ref["ys"], "ys")
     with torch.no_grad():  # the serving call keeps no z
         y1 = L.expert_linear(leaves[0], leaves[1], plan, bias=leaves[2] if bias else None, activation=act)
@@ -265,6 +265,18 @@ SIZES = [
 @pytest.mark.parametrize("act", ["none", "silu"])
 def test_products(dtype, T, m, E, K, F, act):
     check_product(dtype, T, m, E, K, F, act, idle=(1,) if E > 3 else ())
+
+
+# enough rows for every tile size, ends inside the tiles, and widths off 16
+# bytes; the float64 reference runs on the GPU
+LARGE = [(2000, 2, 12, 520, 520), (8000, 2, 5, 1032, 4104), (4000, 2, 8, 1001, 2001), (1500, 2, 4, 1024, 513),
+         (700, 2, 5, 2056, 264)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,m,E,K,F", LARGE)
+def test_products_of_many_rows(dtype, T, m, E, K, F):
+    check_product(dtype, T, m, E, K, F, "silu", idle=(2,), on="cuda")
 
 
 @pytest.mark.parametrize("dtype", TYPES)
