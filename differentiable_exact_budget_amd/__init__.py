@@ -14,13 +14,13 @@ import torch
 from ._binding import (PATH_AUTO, PATH_BRACKET, PATH_FORCE_FALLBACK, PATH_FULL, LapsumError, Options, Stats,
                        default_options, lib)
 from .experts import (ExpertPlan, expert_combine, expert_combine_vjp, expert_dispatch, expert_dispatch_vjp,
-                      expert_linear, expert_linear_vjp, expert_sort, expert_topk, expert_topk_vjp)
+                      expert_linear, expert_linear_forward, expert_linear_vjp, expert_sort, expert_topk, expert_topk_vjp)
 
 __all__ = ["forward", "vjp", "vjp_kt", "soft_topk", "topk_threshold", "hard_topk", "dftopk",
            "forward_rows", "vjp_rows", "soft_topk_rows", "SoftTopK", "default_options", "Options", "Stats", "LapsumError",
-           "PATH_AUTO", "PATH_FULL", "PATH_BRACKET", "PATH_FORCE_FALLBACK", "release_workspaces", "ExpertPlan", "expert_topk", "expert_topk_vjp",
-           "expert_sort", "expert_dispatch", "expert_dispatch_vjp", "expert_linear", "expert_linear_vjp",
-           "expert_combine", "expert_combine_vjp"]
+           "PATH_AUTO", "PATH_FULL", "PATH_BRACKET", "PATH_FORCE_FALLBACK", "release_workspaces",
+           "ExpertPlan", "expert_topk", "expert_topk_vjp", "expert_sort", "expert_dispatch", "expert_dispatch_vjp",
+           "expert_linear", "expert_linear_forward", "expert_linear_vjp", "expert_combine", "expert_combine_vjp"]
 
 
 def _check_scores(x: torch.Tensor, name: str) -> None:

@@ -1,6 +1,7 @@
-"""Build the gfx950 HIP library liblapsum.so in-tree with hipcc.
+"""Build the gfx950 HIP library liblapsum.so in-tree with hipcc, and with g++
+the torch module of the expert operators (_experts_torch.so, host code only).
 
-Every source is compiled as HIP for gfx950 only; packed-fp32 instruction
+Every HIP source is compiled for gfx950 only; packed-fp32 instruction
 selection is disabled (-Xclang -target-feature -Xclang -packed-fp32-ops).
 """
 import concurrent.futures as cf
@@ -13,6 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 OUT = os.path.join(HERE, "liblapsum.so")
 BUILD = os.path.join(ROOT, "_build")
+TORCH_SOURCE = "experts_torch.cpp"
+TORCH_OUT = os.path.join(HERE, "_experts_torch.so")
 
 SOURCES = ["lapsum_sample.hip", "lapsum_stream.hip", "lapsum_sort.hip", "lapsum_ceiling.hip", "lapsum_topk.hip", "lapsum_batched.hip", "lapsum_heavy.hip", "lapsum_noalloc.hip", "lapsum_route.hip", "lapsum_tokens.hip",
            "lapsum_expert_linear.hip", "lapsum_expert_mfma.hip", "lapsum_expert_few.hip",
@@ -43,10 +46,44 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _run(cmd, what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stderr}")
+
+
+def _compile_torch(verbose: bool) -> str:
+    """The torch module's object, with the headers of the torch in use."""
+    import torch
+    import sysconfig
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, TORCH_SOURCE + ".o")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], "/opt/rocm/include", os.path.join(ROOT, "include")]
+    _run(["g++", "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj, "-O2", "-std=c++17", "-fPIC", "-w",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-DTORCH_EXTENSION_NAME=_experts_torch",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+         + [f for d in inc for f in ("-isystem", d)], f"g++ on {TORCH_SOURCE}", verbose)
+    return obj
+
+
+def _link_torch(obj: str, verbose: bool) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run(["g++", "-shared", "-o", TORCH_OUT + ".tmp", obj, "-L" + HERE, "-l:liblapsum.so", "-L" + libs, "-lc10",
+          "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of the torch module",
+         verbose)
+    os.replace(TORCH_OUT + ".tmp", TORCH_OUT)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+        torch_obj = ex.submit(_compile_torch, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        torch_obj = torch_obj.result()
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", "-o", OUT + ".tmp"] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -54,6 +91,7 @@ def build(verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(OUT + ".tmp", OUT)
+    _link_torch(torch_obj, verbose)
     return OUT
 
 

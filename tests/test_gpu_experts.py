@@ -424,6 +424,44 @@ def test_refusals():
             f()
 
 
+def test_only_what_requires_a_gradient_gets_one():
+    T, m, E, K, F = 20, 2, 4, 16, 24
+    plan, o, order, place = make_plan(some_ids(T, m, E, 1), E)
+    g = gen(2)
+    xs = torch.randn(T * m, K, generator=g).cuda()
+    wt, b = torch.randn(E, F, K, generator=g).cuda(), torch.randn(E, F, generator=g).cuda()
+    dy = torch.randn(T * m, F, generator=g).cuda()
+    _, z = L.expert_linear_forward(xs, wt, plan, bias=b, activation="silu")
+    want = L.expert_linear_vjp(xs, wt, plan, z, dy, activation="silu")
+    for i in range(3):
+        leaves = [t.detach().requires_grad_(i == j) for j, t in enumerate((xs, wt, b))]
+        y = L.expert_linear(leaves[0], leaves[1], plan, bias=leaves[2], activation="silu")
+        y.backward(dy)
+        for j, t in enumerate(leaves):
+            assert (t.grad is None) == (i != j)
+        assert torch.equal(leaves[i].grad, want[i])
+        alone = L.expert_linear_vjp(xs, wt, plan, z, dy, activation="silu", want=[i == j for j in range(3)])
+        assert [t is None for t in alone] == [i != j for j in range(3)]
+    x = torch.randn(T, F, generator=g).cuda()
+    w = torch.rand(T, m, generator=g).cuda()
+    both = L.expert_combine_vjp(dy, w, plan, x)
+    for i in range(3):
+        ys, wd, res = (t.detach().requires_grad_(i == j) for j, t in enumerate((dy, w, torch.zeros_like(x))))
+        L.expert_combine(ys, wd, plan, residual=res).backward(x)
+        for j, t in enumerate((ys, wd, res)):
+            assert (t.grad is None) == (i != j)
+            if i == j:
+                assert torch.equal(t.grad, x if j == 2 else both[j])
+
+
+def test_second_derivatives_are_refused():
+    plan, *_ = make_plan(some_ids(6, 2, 3, 1), 3)
+    x = torch.randn(6, 8, device="cuda", requires_grad=True)
+    y = L.expert_dispatch(x, plan)
+    with pytest.raises(RuntimeError, match="twice"):
+        torch.autograd.grad(y.sum(), x, create_graph=True)
+
+
 def test_a_plan_from_elsewhere_stays_in_bounds():
     """Places and offsets outside the pairs are empty slots and clamped ends."""
     T, m, E, D = 6, 2, 3, 32
