@@ -192,7 +192,13 @@ __global__ __launch_bounds__(kAnyThreads) void k_product_any(LinearArgs g, long 
     __shared__ __align__(128) char lds[2 * kAnySteps * 2 * B * 64 * (SPLIT ? 4 : 1)];
     for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
         // tiles past the last (their number is only bounded here) have no rows
-        const Place<T> at = find_place<T, FORM, B>(g, (int)t, cols);
+        Place<T> at;
+        if constexpr (FORM == kFormDw) {
+            at = dw_place<T, B>(g, (int)t, cols);
+        } else {
+            RowTiles<B> rows(g.off, g.E, g.P);
+            at = row_place<T, FORM, B>(g, rows, (int)t, cols);
+        }
         if (at.rows > 0 && at.q < at.rows * cols)
             any_tile<T, FORM, ACT, B, SPLIT>(at.p, at.q / cols * B, at.q % cols * B, lds);
         __syncthreads();

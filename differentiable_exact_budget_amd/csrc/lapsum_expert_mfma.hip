@@ -201,7 +201,7 @@ LS_DEV void form_tile(const Piece<T>& p, int i0, int j0, char* lds) {
             step(std::integral_constant<int, 0>{}, k0);
             step(std::integral_constant<int, 1>{}, k0 + kStepK);
         }
-        // nothing may land in LDS after this, or in registers' stead
+        // the last steps' loads, past K, still write zeros to LDS
         step_barrier<0>();
     }
     // lane l holds row l % 16 of a fragment and, of a pair of fragments,
@@ -269,24 +269,32 @@ __global__ __launch_bounds__(kProductThreads) void k_product(LinearArgs g) {
     constexpr bool kCut = BM == 256;
     __shared__ __align__(1024) char lds[kRing * (BM + BN) * kStepK * 2];
     const int cols = ((FORM == kFormY ? g.out : g.in) + BN - 1) / BN;
-    const int tiles = FORM == kFormDw ? (g.out + BM - 1) / BM * g.E : count_row_tiles<BM>(g.off, g.E, g.P);
-    const Turn t = take_turn(blockIdx.x, tiles * cols, kCut);
-    if (t.tile < 0) return;
-    const Place<T> at = find_place<T, FORM, BM>(g, t.tile, cols);
-    const Piece<T>& p = at.p;
-    const int q = at.q, rows = at.rows, quarter = t.quarter;
-    const int first = q / (kGroup * cols) * kGroup, n = min(kGroup, rows - first);
-    const int in = q - first * cols;
+    Place<T> at;
+    int quarter;
+    if constexpr (FORM == kFormDw) {
+        const Turn t = take_turn(blockIdx.x, (g.out + BM - 1) / BM * g.E * cols, kCut);
+        if (t.tile < 0) return;
+        at = dw_place<T, BM>(g, t.tile, cols);
+        quarter = t.quarter;
+    } else {
+        RowTiles<BM> rows(g.off, g.E, g.P);
+        const Turn t = take_turn(blockIdx.x, rows.count() * cols, kCut);
+        if (t.tile < 0) return;
+        at = row_place<T, FORM, BM>(g, rows, t.tile, cols);
+        quarter = t.quarter;
+    }
+    const int first = at.q / (kGroup * cols) * kGroup, n = min(kGroup, at.rows - first);
+    const int in = at.q - first * cols;
     int i0 = (first + in % n) * BM, j0 = in / n * BN;
     if constexpr (kCut) {
         if (quarter >= 0) {
             i0 += (quarter >> 1) * (BM / 2);
             j0 += (quarter & 1) * (BN / 2);
-            if (i0 < p.M && j0 < p.N) form_tile<T, FORM, ACT, BM / 2, BN / 2>(p, i0, j0, lds);
+            if (i0 < at.p.M && j0 < at.p.N) form_tile<T, FORM, ACT, BM / 2, BN / 2>(at.p, i0, j0, lds);
             return;
         }
     }
-    form_tile<T, FORM, ACT, BM, BN>(p, i0, j0, lds);
+    form_tile<T, FORM, ACT, BM, BN>(at.p, i0, j0, lds);
 }
 
 template <class T, int B>

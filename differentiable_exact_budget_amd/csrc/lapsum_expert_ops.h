@@ -97,6 +97,12 @@ void launch_expert_dbias(const float* part, int dtype, const int32_t* off, int P
 #if defined(__HIPCC__)
 
 LS_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <class T>
+LS_DEV T* uniform(T* p) {
+    const uintptr_t u = reinterpret_cast<uintptr_t>(p);
+    const uint32_t lo = (uint32_t)uniform((int)(uint32_t)u), hi = (uint32_t)uniform((int)(uint32_t)(u >> 32));
+    return reinterpret_cast<T*>((uintptr_t)hi << 32 | lo);
+}
 LS_DEV float wave_sum_f32(float v) {
     v += __uint_as_float(xor_lane<32>(__float_as_uint(v)));
     v += __uint_as_float(xor_lane<16>(__float_as_uint(v)));
@@ -110,45 +116,64 @@ LS_DEV float wave_sum_f32(float v) {
 // offsets[e] as a row number: a plan from elsewhere is kept in bounds
 LS_DEV int row_at(const int32_t* __restrict__ off, int e, int P) { return min(max(off[e], 0), P); }
 
-// Tile `tile` of the rows cut into tiles of BM that never cross an expert:
-// its expert and rows [lo, hi).  Behind the last expert's tiles come those of
-// the unused rows (e = E).  `first` is the expert's first tile.  A tile past
-// the end has lo = hi = P.  Every lane of the wave calls it with one `tile`.
+// The rows cut into tiles of BM that never cross an expert, the experts' tiles
+// in order and those of the unused rows (e = E) behind them.  Lane l holds
+// expert e0 + l of 64 experts; with more, find() goes through them again.
+// Every lane of a wave calls these with one tile.
 struct RowTile {
-    int e, lo, hi, first;
+    int e;         // expert, or E
+    int lo, hi;    // the tile's rows; a tile past the last has lo = hi = P
+    int first;     // the expert's first tile
+    int elo, ehi;  // the expert's rows
+};
+template <int BM>
+struct RowTiles {
+    const int32_t* off;
+    int E, P;
+    int lo, hi, inc;  // this lane's expert: its rows, and the tiles up to it
+
+    LS_DEV void load(int e0) {
+        const int e = e0 + lane_id();
+        lo = e < E ? row_at(off, e, P) : 0;
+        hi = e < E ? max(row_at(off, e + 1, P), lo) : 0;
+        inc = (int)wave_inclusive_scan((uint32_t)((hi - lo + BM - 1) / BM));
+    }
+    LS_DEV RowTiles(const int32_t* __restrict__ off_, int E_, int P_) : off(off_), E(E_), P(P_) { load(0); }
+
+    LS_DEV RowTile find(int tile) {
+        int base = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            if (E > 64) load(e0);
+            const unsigned long long hit = ballot(base + inc > tile);
+            if (hit) {
+                const int f = __builtin_ctzll(hit);
+                RowTile t;
+                t.e = e0 + f;
+                t.elo = __builtin_amdgcn_readlane(lo, f);
+                t.ehi = __builtin_amdgcn_readlane(hi, f);
+                t.first = base + __builtin_amdgcn_readlane(inc, f) - (t.ehi - t.elo + BM - 1) / BM;
+                t.lo = t.elo + (tile - t.first) * BM;
+                t.hi = min(t.lo + BM, t.ehi);
+                return t;
+            }
+            base += __builtin_amdgcn_readlane(inc, 63);
+        }
+        const int used = uniform(row_at(off, E, P));
+        const int at = (int)min((long long)used + (long long)(tile - base) * BM, (long long)P);
+        return {E, at, min(at + BM, P), base, used, P};
+    }
+    LS_DEV int count() {
+        int n = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            if (E > 64) load(e0);
+            n += __builtin_amdgcn_readlane(inc, 63);
+        }
+        return n + (P - uniform(row_at(off, E, P)) + BM - 1) / BM;
+    }
 };
 template <int BM>
 LS_DEV RowTile find_row_tile(const int32_t* __restrict__ off, int E, int P, int tile) {
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane_id();
-        int lo = 0, n = 0;
-        if (e < E) {
-            lo = row_at(off, e, P);
-            n = (max(row_at(off, e + 1, P) - lo, 0) + BM - 1) / BM;
-        }
-        const int inc = (int)wave_inclusive_scan((uint32_t)n);
-        const unsigned long long hit = __ballot(base + inc > tile);
-        if (hit) {
-            const int f = __builtin_ctzll(hit);
-            const int first = base + __builtin_amdgcn_readlane(inc, f) - __builtin_amdgcn_readlane(n, f);
-            const int r0 = __builtin_amdgcn_readlane(lo, f) + (tile - first) * BM;
-            const int r1 = uniform(row_at(off, e0 + f + 1, P));
-            return {e0 + f, r0, min(r0 + BM, r1), first};
-        }
-        base += __builtin_amdgcn_readlane(inc, 63);
-    }
-    const long long r0 = (long long)uniform(row_at(off, E, P)) + (long long)(tile - base) * BM;
-    const int lo = (int)min(r0, (long long)P);
-    return {E, lo, min(lo + BM, P), base};
-}
-// number of tiles of the experts and of the unused rows
-template <int BM>
-LS_DEV int count_row_tiles(const int32_t* __restrict__ off, int E, int P) {
-    int n = 0;
-    for (int e = lane_id(); e < E; e += 64) n += (max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + BM - 1) / BM;
-    n = __builtin_amdgcn_readlane((int)wave_inclusive_scan((uint32_t)n), 63);
-    return n + (P - uniform(row_at(off, E, P)) + BM - 1) / BM;
+    return RowTiles<BM>(off, E, P).find(tile);
 }
 // most tiles there can be (host)
 template <int BM>

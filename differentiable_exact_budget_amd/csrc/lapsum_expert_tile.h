@@ -93,51 +93,55 @@ struct Piece {
     typename ZKeep<T>::type* z;
     int M, N, K, lda, ldb, ldc;
 };
-// Where in its piece a tile lies, in tiles: `first` of the piece's row tiles
-// `rows`, and its number among them, `q`.
+// A piece, the number of its row tiles, and a tile's number in it.
 template <class T>
 struct Place {
     Piece<T> p;
     int q, rows;
 };
 
-// The piece of tile t of the product, `cols` tiles wide.
+// The piece of tile t of a row form, in tiles of BM rows and `cols` columns.
 template <class T, int FORM, int BM>
-LS_DEV Place<T> find_place(const LinearArgs& g, int t, int cols) {
+LS_DEV Place<T> row_place(const LinearArgs& g, RowTiles<BM>& tiles, int t, int cols) {
     Place<T> r;
     Piece<T>& p = r.p;
+    const RowTile at = tiles.find(t / cols);
+    const bool used = at.e < g.E;
+    p.M = at.ehi - at.elo;
     p.N = FORM == kFormY ? g.out : g.in;
+    p.K = !used ? 0 : FORM == kFormY ? g.in : g.out;  // unused rows: zeros
+    p.lda = FORM == kFormY ? g.in : g.out;
+    p.ldb = g.in;
     p.ldc = p.N;
+    p.a = (const T*)g.a + (long long)at.elo * p.lda;
+    p.b = (const T*)g.b + (long long)(used ? at.e : 0) * g.out * g.in;
+    p.c = (T*)g.c + (long long)at.elo * p.N;
+    p.bias = FORM == kFormY && g.bias && used ? (const T*)g.bias + (long long)at.e * g.out : nullptr;
+    p.z = FORM == kFormY && g.z && used ? (typename ZKeep<T>::type*)g.z + (long long)at.elo * p.N : nullptr;
+    r.rows = (p.M + BM - 1) / BM;
+    r.q = t - at.first * cols;
+    return r;
+}
+// the same of the weight gradient
+template <class T, int BM>
+LS_DEV Place<T> dw_place(const LinearArgs& g, int t, int cols) {
+    Place<T> r;
+    Piece<T>& p = r.p;
+    r.rows = (g.out + BM - 1) / BM;
+    const int e = t / (r.rows * cols);
+    r.q = t % (r.rows * cols);
+    const int lo = uniform(row_at(g.off, e, g.P));
+    p.M = g.out;
+    p.N = g.in;
+    p.K = max(uniform(row_at(g.off, e + 1, g.P)) - lo, 0);
+    p.lda = g.out;
+    p.ldb = g.in;
+    p.ldc = g.in;
+    p.a = (const T*)g.a + (long long)lo * g.out;
+    p.b = (const T*)g.b + (long long)lo * g.in;
+    p.c = (T*)g.c + (long long)e * g.out * g.in;
     p.bias = nullptr;
     p.z = nullptr;
-    p.ldb = g.in;
-    if (FORM == kFormDw) {
-        r.rows = (g.out + BM - 1) / BM;
-        const int e = t / (r.rows * cols);
-        r.q = t % (r.rows * cols);
-        const int lo = uniform(row_at(g.off, e, g.P));
-        p.K = max(uniform(row_at(g.off, e + 1, g.P)) - lo, 0);
-        p.M = g.out, p.lda = g.out;
-        p.a = (const T*)g.a + (long long)lo * g.out;
-        p.b = (const T*)g.b + (long long)lo * g.in;
-        p.c = (T*)g.c + (long long)e * g.out * g.in;
-    } else {
-        const RowTile at = find_row_tile<BM>(g.off, g.E, g.P, t / cols);
-        const int lo = uniform(row_at(g.off, at.e, g.P));
-        const int hi = at.e < g.E ? max(uniform(row_at(g.off, at.e + 1, g.P)), lo) : g.P;
-        p.M = hi - lo;
-        r.rows = (p.M + BM - 1) / BM;
-        r.q = t - at.first * cols;
-        p.K = at.e == g.E ? 0 : FORM == kFormY ? g.in : g.out;  // unused rows: zeros
-        p.lda = FORM == kFormY ? g.in : g.out;
-        p.a = (const T*)g.a + (long long)lo * p.lda;
-        p.b = (const T*)g.b + (long long)(at.e < g.E ? at.e : 0) * g.out * g.in;
-        p.c = (T*)g.c + (long long)lo * p.N;
-        if (FORM == kFormY && at.e < g.E) {
-            if (g.bias) p.bias = (const T*)g.bias + (long long)at.e * g.out;
-            if (g.z) p.z = (typename ZKeep<T>::type*)g.z + (long long)lo * p.N;
-        }
-    }
     return r;
 }
 
