@@ -16,7 +16,11 @@
 namespace lapsum {
 
 constexpr int kAnyThreads = 256;
-constexpr int kAnySteps = 2;  // steps of 64 bytes of k in a buffer
+
+// steps of 64 bytes of k in a buffer (split, 513 x 2 rows of 257 -> 1001 in
+// fp32, one / two: y 16.6 / 21.6 us, dx 18.6 / 18.6, dW 14.1 / 19.5: 32 KB of
+// LDS leave room for five workgroups on a CU, 64 KB for two)
+constexpr int any_steps(bool split) { return split ? 1 : 2; }
 
 // One operand: R rows by one step of k, dealt out to NT threads in chunks.
 template <class T, int R, bool KFAST, bool PAIRED, int NT>
@@ -76,6 +80,7 @@ LS_DEV void any_tile(const Piece<T>& p, int i0, int j0, char* lds) {
     constexpr int NT = SPLIT ? 64 : kAnyThreads;
     using OpA = AnyOperand<T, B, kA, false, NT>;
     using OpB = AnyOperand<T, B, kB, k16, NT>;
+    constexpr int kAnySteps = any_steps(SPLIT);
     constexpr int kStepK = OpA::kStepK, kDeep = kAnySteps * kStepK;
     constexpr int kBuffer = kAnySteps * (OpA::kBytes + OpB::kBytes);
     constexpr int W = SPLIT ? B : B / 2;         // a wave's rows and columns
@@ -189,7 +194,7 @@ LS_DEV void any_tile(const Piece<T>& p, int i0, int j0, char* lds) {
 
 template <class T, int FORM, int ACT, int B, bool SPLIT>
 __global__ __launch_bounds__(kAnyThreads) void k_product_any(LinearArgs g, long long tiles, int cols) {
-    __shared__ __align__(128) char lds[2 * kAnySteps * 2 * B * 64 * (SPLIT ? 4 : 1)];
+    __shared__ __align__(128) char lds[2 * any_steps(SPLIT) * 2 * B * 64 * (SPLIT ? 4 : 1)];
     for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
         // tiles past the last (their number is only bounded here) have no rows
         Place<T> at;
@@ -263,8 +268,9 @@ LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const
     const int l = lane_id(), w = threadIdx.x >> 6;
     const long long c = (long long)tj * (64 * V) + l * V;
     float sum[V] = {};
-    // four rows' loads are in flight at a time
-    constexpr int U = 4;
+    // U rows' loads are in flight at a time (V = 1, 1026 rows of 1001: 12.4 us
+    // with 4, 11.5 with 16)
+    constexpr int U = V == 1 ? 16 : 4;
     struct __attribute__((aligned(sizeof(T) * V))) PT {
         T v[V];
     };

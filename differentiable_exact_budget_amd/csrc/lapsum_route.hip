@@ -14,17 +14,24 @@ namespace lapsum {
 // ---------------------------------------------------------------------------
 // the m largest gates of every row
 // ---------------------------------------------------------------------------
-// A row lies in 16 lanes, V gates each (expert lane + 16 i), four rows to a
-// wave.  A gate's key is 64 bits: its order-preserving 32-bit key above
-// 1023 - expert, so keys differ and the larger of two equal gates is the one
-// of the lower expert.  Keys are below 2^62 and positive, so they order alike
-// as doubles, and the double maximum and compare take one instruction each
-// where integers take several.  Each of m rounds takes the row's largest key
-// (over a lane's keys, then over the 16 lanes) and blanks it; a key without
-// its upper half is below every gate's.  V is E / 16 rounded up to few sizes.
-// Vector instructions bound it: about 3 V + 20 a round for four rows
-// (65536 rows of 257 gates, m = 8: 17 us; with 32-bit keys, a second search
-// for the expert and a compare to blank it, 40 us).
+// A row lies in 16 lanes (expert e in lane e % 16), four rows to a wave.  A
+// gate's key is 64 bits: its order-preserving 32-bit key above 1023 - expert,
+// so keys differ and the larger of two equal gates is the one of the lower
+// expert.  Keys are below 2^62 and positive, so they order alike as doubles,
+// and the double maximum takes one instruction where integers take several.  A
+// key without its upper half is below every gate's.
+//
+// Each of m rounds takes the largest of the 16 lanes' largest keys, blanks it,
+// and finds its lane's next one.  Up to 192 experts a lane's keys are in
+// registers and every lane searches its own again; with more, where only the
+// one lane's keys have changed, they lie in LDS and the row's 16 lanes search
+// them together.  Vector instructions bound both.  Measured, registers / LDS,
+// us, 2^24 gates in rows of E, of which m are chosen:
+//   E       128            192            257            512            1024
+//   m = 2   16.1 / 16.7    15.6 / 16.9    16.4 / 17.4    16.7 / 14.8    32.6 / 22.6
+//   m = 8   28.4 / 29.9    26.9 / 26.1    27.8 / 24.9    26.8 / 20.4    50.6 / 28.1
+//   m = 32  82.6 / 99.2    73.9 / 72.8    74.9 / 59.1    67.6 / 42.2     122 / 49.5
+// (the 67 MB of gates take 13 us).
 constexpr int kTopkLanes = 16;
 constexpr int kTopkThreads = 256;
 static_assert(kExpertsMax <= 1024, "an expert has 10 bits of a key");
@@ -42,72 +49,132 @@ LS_DEV double max16(double v) {
     return max_f64(v, xor_lane_f64<1>(v));
 }
 
-template <int V>
-LS_DEV void topk_row(const float* __restrict__ gates, long long row, long long T, int E, int m, float floor,
-                     int32_t* __restrict__ ids, float* __restrict__ w, float* __restrict__ sums) {
-    const int l = threadIdx.x & (kTopkLanes - 1);
-    const bool live = row < T;
-    const float* g = gates + (live ? row : T - 1) * E;
-    double key[V];
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = l + kTopkLanes * i < E ? g[l + kTopkLanes * i] : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t k = f2key(v[i]);
-        const unsigned long long q = ((unsigned long long)k << 30) | (uint32_t)(1023 - (l + kTopkLanes * i));
-        key[i] = v[i] > floor ? __longlong_as_double((long long)q) : 0.0;
-    }
-    constexpr int kBlocks = kSlotsMax / kTopkLanes;
+// the key of expert e's gate from its 32-bit key; 0: not to be chosen
+LS_DEV double wide_key(uint32_t k, int e) {
+    const unsigned long long q = ((unsigned long long)k << 30) | (uint32_t)(1023 - e);
+    return k ? __longlong_as_double((long long)q) : 0.0;
+}
+LS_DEV uint32_t gate_key(float v, float floor) { return v > floor ? f2key(v) : 0u; }
+
+// What a row's 16 lanes collect: slot 16 b + l in lane l.
+struct TopkRow {
+    static constexpr int kBlocks = kSlotsMax / kTopkLanes;
     int id[kBlocks];
     float wt[kBlocks];
     float sum = 0.0f;
+
+    // runs the m rounds; next(some, e) gives this lane's largest key once
+    // expert e's is blanked
+    template <class F>
+    LS_DEV void collect(double mine, int m, F&& next) {
+        const int l = threadIdx.x & (kTopkLanes - 1);
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-        id[b] = -1;
-        wt[b] = 0.0f;
-        for (int j = 0; j < kTopkLanes && b * kTopkLanes + j < m; ++j) {
-            double best = key[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i) best = max_f64(best, key[i]);
-            best = max16(best);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int hi = key[i] == best ? 0 : __double2hiint(key[i]);
-                key[i] = __hiloint2double(hi, __double2loint(key[i]));
-            }
-            const unsigned long long q = (unsigned long long)__double_as_longlong(best);
-            const bool some = (q >> 32) != 0;  // a gate above the floor has a key of at least 2^53
-            const float gate = some ? key2f((uint32_t)(q >> 30)) : 0.0f;
-            sum += gate;
-            if (j == l) {
-                id[b] = some ? 1023 - (int)(q & 1023) : -1;
-                wt[b] = gate;
+        for (int b = 0; b < kBlocks; ++b) {
+            id[b] = -1;
+            wt[b] = 0.0f;
+            for (int j = 0; j < kTopkLanes && b * kTopkLanes + j < m; ++j) {
+                const double best = max16(mine);
+                const unsigned long long q = (unsigned long long)__double_as_longlong(best);
+                const bool some = (q >> 32) != 0;  // a gate above the floor has a key of at least 2^53
+                const int e = 1023 - (int)(q & 1023);
+                const float gate = some ? key2f((uint32_t)(q >> 30)) : 0.0f;
+                sum += gate;
+                if (j == l) {
+                    id[b] = some ? e : -1;
+                    wt[b] = gate;
+                }
+                mine = next(best, some, e);
             }
         }
     }
-    if (!live) return;
-    if (sums) {
+    LS_DEV void store(long long row, int m, int32_t* __restrict__ ids, float* __restrict__ w,
+                      float* __restrict__ sums) {
+        const int l = threadIdx.x & (kTopkLanes - 1);
+        if (sums && l == 0) sums[row] = sum;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) wt[b] = sum > 0.0f ? wt[b] / sum : 0.0f;
-        if (l == 0) sums[row] = sum;
-    }
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-        const int j = b * kTopkLanes + l;
-        if (j < m) {
+        for (int b = 0; b < kBlocks; ++b) {
+            const int j = b * kTopkLanes + l;
+            if (j >= m) continue;
             ids[row * m + j] = id[b];
-            w[row * m + j] = wt[b];
+            w[row * m + j] = !sums ? wt[b] : sum > 0.0f ? wt[b] / sum : 0.0f;
         }
     }
-}
+};
+
+// V keys a lane, in registers
 template <int V>
 __global__ __launch_bounds__(kTopkThreads) void k_expert_topk(const float* __restrict__ gates, long long T, int E,
                                                                int m, float floor, int32_t* __restrict__ ids,
                                                                float* __restrict__ w, float* __restrict__ sums) {
     constexpr int kRows = kTopkThreads / kTopkLanes;
-    for (long long row0 = (long long)blockIdx.x * kRows; row0 < T; row0 += (long long)gridDim.x * kRows)
-        topk_row<V>(gates, row0 + threadIdx.x / kTopkLanes, T, E, m, floor, ids, w, sums);
+    const int l = threadIdx.x & (kTopkLanes - 1);
+    for (long long row0 = (long long)blockIdx.x * kRows; row0 < T; row0 += (long long)gridDim.x * kRows) {
+        const long long row = row0 + threadIdx.x / kTopkLanes;
+        const float* g = gates + min(row, T - 1) * E;
+        double key[V];
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = l + kTopkLanes * i < E ? g[l + kTopkLanes * i] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = wide_key(gate_key(v[i], floor), l + kTopkLanes * i);
+        auto largest = [&] {
+            double k = key[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) k = max_f64(k, key[i]);
+            return k;
+        };
+        TopkRow r;
+        r.collect(largest(), m, [&](double best, bool, int) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                key[i] = __hiloint2double(key[i] == best ? 0 : __double2hiint(key[i]), __double2loint(key[i]));
+            return largest();
+        });
+        if (row < T) r.store(row, m, ids, w, sums);
+    }
+}
+
+// the 32-bit keys of a workgroup's rows in LDS (E words a row)
+__global__ __launch_bounds__(kTopkThreads) void k_expert_topk_lds(const float* __restrict__ gates, long long T, int E,
+                                                                   int m, float floor, int32_t* __restrict__ ids,
+                                                                   float* __restrict__ w, float* __restrict__ sums) {
+    extern __shared__ uint32_t lds_keys[];
+    constexpr int kRows = kTopkThreads / kTopkLanes;
+    const int l = threadIdx.x & (kTopkLanes - 1);
+    uint32_t* keys = lds_keys + threadIdx.x / kTopkLanes * E;
+    for (long long row0 = (long long)blockIdx.x * kRows; row0 < T; row0 += (long long)gridDim.x * kRows) {
+        const long long row = row0 + threadIdx.x / kTopkLanes;
+        const float* g = gates + min(row, T - 1) * E;
+        double mine = 0.0;
+        constexpr int U = 8;  // loads in flight a lane
+        for (int e0 = l; e0 < E; e0 += U * kTopkLanes) {
+            float v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) v[i] = e0 + kTopkLanes * i < E ? g[e0 + kTopkLanes * i] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = e0 + kTopkLanes * i;
+                const uint32_t k = gate_key(v[i], floor);
+                if (e < E) keys[e] = k;
+                mine = max_f64(mine, wide_key(k, e & 1023));
+            }
+        }
+        TopkRow r;
+        r.collect(mine, m, [&](double, bool some, int e) {
+            // a row's keys are written and read by one wave, whose LDS
+            // operations are served in order
+            const int from = e & (kTopkLanes - 1);
+            if (some && l == from) keys[e] = 0u;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            double k = 0.0;
+            for (int o = from + kTopkLanes * l; o < E; o += kTopkLanes * kTopkLanes) k = max_f64(k, wide_key(keys[o], o));
+            k = max16(k);
+            if (l == from) mine = k;
+            return mine;
+        });
+        if (row < T) r.store(row, m, ids, w, sums);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
 }
 
 void launch_expert_topk(const float* gates, long long T, int E, int m, float floor, int32_t* ids, float* w,
@@ -120,9 +187,10 @@ void launch_expert_topk(const float* gates, long long T, int E, int m, float flo
         hipLaunchKernelGGL((k_expert_topk<V>), grid, block, 0, st, gates, T, E, m, floor, ids, w, sums);    \
         return;                                                                                             \
     }
-    LS_TOPK(1) LS_TOPK(2) LS_TOPK(3) LS_TOPK(4) LS_TOPK(6) LS_TOPK(8) LS_TOPK(10) LS_TOPK(12) LS_TOPK(14) LS_TOPK(16)
-    LS_TOPK(18) LS_TOPK(20) LS_TOPK(24) LS_TOPK(28) LS_TOPK(32) LS_TOPK(40) LS_TOPK(48) LS_TOPK(64)
+    LS_TOPK(1) LS_TOPK(2) LS_TOPK(3) LS_TOPK(4) LS_TOPK(6) LS_TOPK(8) LS_TOPK(12)
 #undef LS_TOPK
+    hipLaunchKernelGGL(k_expert_topk_lds, grid, block, sizeof(uint32_t) * (size_t)E * (kTopkThreads / kTopkLanes), st,
+                       gates, T, E, m, floor, ids, w, sums);
 }
 
 // ---------------------------------------------------------------------------
@@ -190,17 +258,20 @@ void launch_expert_topk_vjp(const int32_t* ids, const float* w, const float* dw,
 // expert's base + the pairs of earlier waves + those of its own wave's
 // earlier runs + those of lower lanes.
 //
-// Up to kSortOneMax pairs one workgroup does it all, in one launch.  More are
-// dealt out in contiguous shares to many: counts per share and expert, their
-// prefix sums over the shares (a wave per expert), and the places.  Launches
-// and LDS latencies bound it, not the 12 bytes a pair (65536 x 8 pairs, 257
-// experts: count 3, scan 3, place 6 us, at 6 TB/s the bytes would take 1).
+// Up to one such tile a workgroup of 16 waves does it all, in one launch (64
+// pairs: 4.8 us, 4096 pairs: 6.3 us).  More are dealt out in contiguous shares
+// to many: counts per share and expert, their prefix sums over the shares (a
+// wave per expert), and the places (one workgroup, tile after tile / many, us:
+// 4097 pairs of 64 experts 9.4 / 10.0, 8192 of 257 14.0 / 10.1, 16384 of 64
+// 20.6 / 9.8).  Launches and LDS latencies bound it, not the 12 bytes a pair:
+// 65536 x 8 pairs of 257 experts take 15 us back to back (count 3.5, scan 3.7,
+// place 8.9), their bytes would take 1.
 constexpr int kPairRuns = 4;
 constexpr int kOneWaves = 16;                       // the single workgroup
 constexpr int kManyWaves = 8;                       // one of many
 constexpr int kPairTile = kManyWaves * 64 * kPairRuns;  // 2048 pairs
 constexpr int kPairBlocksMax = 1024;
-constexpr int kSortOneMax = 4 * kOneWaves * 64 * kPairRuns;  // 16384
+constexpr int kSortOneMax = kOneWaves * 64 * kPairRuns;  // its only tile: 4096 pairs
 
 // ids outside [0, E) have no expert: -1
 LS_DEV int pair_expert(const int32_t* __restrict__ ids, long long i, long long hi, int E) {
@@ -290,43 +361,60 @@ LS_DEV void count_pairs(const int32_t* __restrict__ ids, long long lo, long long
     __syncthreads();
 }
 
-// tot[E] -> exclusive prefix in base[E] (LDS); returns the sum.  A thread
-// takes the experts K t .. K t + K - 1.
+// The experts' pairs tot[E], of which a thread holds K t .. K t + K - 1.
 template <int W>
-LS_DEV uint32_t prefix_experts(const uint32_t* tot, uint32_t* base, int E, uint32_t* scr) {
-    constexpr int K = (kExpertsMax + W * 64 - 1) / (W * 64);
-    const int e0 = threadIdx.x * K;
-    uint32_t v[K], mine = 0, sum = 0;
-#pragma unroll
-    for (int i = 0; i < K; ++i) mine += v[i] = e0 + i < E ? tot[e0 + i] : 0u;
-    uint32_t ex = block_exclusive_scan<W * 64>(mine, &sum, scr);
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        if (e0 + i < E) base[e0 + i] = ex;
-        ex += v[i];
-    }
-    __syncthreads();
-    return sum;
-}
+struct ExpertCounts {
+    static constexpr int K = (kExpertsMax + W * 64 - 1) / (W * 64);
+    uint32_t v[K];
 
-// ranks and places the pairs [lo, hi), base[e] (LDS) = the next place of e
+    LS_DEV void load(const uint32_t* tot, int E, size_t stride = 1) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int e = threadIdx.x * K + i;
+            v[i] = e < E ? tot[e * stride] : 0u;
+        }
+    }
+    // base[E] (LDS) = exclusive prefix + the thread's own more.v; returns the sum
+    LS_DEV uint32_t prefix(const ExpertCounts& more, uint32_t* base, int E, uint32_t* scr) const {
+        uint32_t mine = 0, sum = 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) mine += v[i];
+        uint32_t ex = block_exclusive_scan<W * 64>(mine, &sum, scr);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int e = threadIdx.x * K + i;
+            if (e < E) base[e] = ex + more.v[i];
+            ex += v[i];
+        }
+        __syncthreads();
+        return sum;
+    }
+};
+
+// One tile of pairs: rank() needs nothing but the ids, place() the experts'
+// bases in LDS (the next place of each, moved past the tile).
 template <int W>
-LS_DEV void place_pairs(const int32_t* __restrict__ ids, long long lo, long long hi, int E, int bits, uint32_t* cnt,
-                        uint32_t* base, int32_t* __restrict__ order, int32_t* __restrict__ place) {
-    const int w = threadIdx.x >> 6;
-    for (long long t = lo; t < hi; t += W * 64 * kPairRuns) {
+struct PairTile {
+    static constexpr int kPairs = W * 64 * kPairRuns;
+    PairRuns r;
+    long long at;
+
+    LS_DEV void rank(const int32_t* __restrict__ ids, long long lo, long long hi, int E, int bits, uint32_t* cnt) {
+        const int w = threadIdx.x >> 6;
         for (int i = threadIdx.x; i < W * E; i += W * 64) cnt[i] = 0u;
         __syncthreads();
-        const long long at = t + (long long)w * (64 * kPairRuns);
-        PairRuns r;
+        at = lo + (long long)w * (64 * kPairRuns);
         rank_runs(ids, at, hi, E, bits, cnt + w * E, r);
         __syncthreads();
+    }
+    LS_DEV void place(long long hi, int E, uint32_t* cnt, uint32_t* base, int32_t* __restrict__ order,
+                      int32_t* __restrict__ to) {
         spread_counts<W>(cnt, base, E);
         __syncthreads();
-        place_runs(r, at, hi, cnt + w * E, order, place);
+        place_runs(r, at, hi, cnt + (threadIdx.x >> 6) * E, order, to);
         __syncthreads();
     }
-}
+};
 
 LS_DEV void write_offsets(const uint32_t* base, uint32_t used, int E, int32_t* __restrict__ offsets) {
     for (int e = threadIdx.x; e < E; e += blockDim.x) offsets[e] = (int32_t)base[e];
@@ -338,12 +426,23 @@ __global__ __launch_bounds__(kOneWaves * 64) void k_sort_one(const int32_t* __re
                                                               int32_t* __restrict__ order,
                                                               int32_t* __restrict__ place) {
     __shared__ uint32_t cnt[kOneWaves * kExpertsMax], tot[kExpertsMax], base[kExpertsMax], scr[kOneWaves + 2];
-    count_pairs<kOneWaves>(ids, 0, P, E, tot);
-    const uint32_t used = prefix_experts<kOneWaves>(tot, base, E, scr);
+    using Tile = PairTile<kOneWaves>;
+    Tile t;
+    t.rank(ids, 0, P, E, bits, cnt);
+    for (int e = threadIdx.x; e < E; e += kOneWaves * 64) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int w = 0; w < kOneWaves; ++w) n += cnt[w * E + e];
+        tot[e] = n;
+    }
+    __syncthreads();
+    ExpertCounts<kOneWaves> all, none = {};
+    all.load(tot, E);
+    const uint32_t used = all.prefix(none, base, E, scr);
     write_offsets(base, used, E, offsets);
     for (int i = (int)used + threadIdx.x; i < P; i += kOneWaves * 64) order[i] = -1;
-    __syncthreads();
-    place_pairs<kOneWaves>(ids, 0, P, E, bits, cnt, base, order, place);
+    __syncthreads();  // offsets are out before the bases move
+    t.place(P, E, cnt, base, order, place);
 }
 
 // counts[e][b]: workgroup b's pairs of expert e
@@ -379,14 +478,22 @@ __global__ __launch_bounds__(kManyWaves * 64) void k_sort_place(const int32_t* _
                                                                  int32_t* __restrict__ order,
                                                                  int32_t* __restrict__ place) {
     __shared__ uint32_t cnt[kManyWaves * kExpertsMax], base[kExpertsMax], scr[kManyWaves + 2];
-    const uint32_t used = prefix_experts<kManyWaves>(totals, base, E, scr);
-    if (blockIdx.x == 0) write_offsets(base, used, E, offsets);
+    using Tile = PairTile<kManyWaves>;
     const long long lo = (long long)blockIdx.x * per, hi = min(lo + per, P);
+    ExpertCounts<kManyWaves> all, before;  // their loads run beside the ids'
+    all.load(totals, E);
+    before.load(counts + blockIdx.x, E, gridDim.x);
+    Tile t;
+    t.rank(ids, lo, hi, E, bits, cnt);
+    const uint32_t used = all.prefix(before, base, E, scr);
+    if (blockIdx.x == 0) write_offsets(base, used, E, offsets);  // no pairs are before the first
     for (long long i = max(lo, (long long)used) + threadIdx.x; i < hi; i += kManyWaves * 64) order[i] = -1;
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kManyWaves * 64) base[e] += counts[(size_t)e * gridDim.x + blockIdx.x];
-    __syncthreads();
-    place_pairs<kManyWaves>(ids, lo, hi, E, bits, cnt, base, order, place);
+    __syncthreads();  // offsets are out before the bases move
+    t.place(hi, E, cnt, base, order, place);
+    for (long long q = lo + Tile::kPairs; q < hi; q += Tile::kPairs) {
+        t.rank(ids, q, hi, E, bits, cnt);
+        t.place(hi, E, cnt, base, order, place);
+    }
 }
 
 static long long sort_blocks(long long P) {
