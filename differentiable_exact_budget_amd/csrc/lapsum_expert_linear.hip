@@ -22,6 +22,8 @@ constexpr int kAnyThreads = 256;
 // LDS leave room for five workgroups on a CU, 64 KB for two)
 constexpr int any_steps(bool split) { return split ? 1 : 2; }
 
+typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any element
+
 // One operand: R rows by one step of k, dealt out to NT threads in chunks.
 template <class T, int R, bool KFAST, bool PAIRED, int NT>
 struct AnyOperand : StepLds<R, KFAST, PAIRED> {
@@ -31,6 +33,26 @@ struct AnyOperand : StepLds<R, KFAST, PAIRED> {
     static constexpr int kLoads = R * 64 / (NT * 16);     // a thread's chunks per step
     static constexpr int kRow = KFAST ? 4 : R / kPer;     // chunks of a row of memory
 
+    // Where a thread's chunks of k = 0 lie, for fetch(): rows past `own` are
+    // the last one's copies, a chunk that starts past a row's end starts at
+    // its last element.  What they bring goes into sums that nobody stores.
+    const T* at[kLoads];
+    LS_DEV void place(const T* __restrict__ x, long long ld, int own, int tid) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int q = i * NT + tid, line = q / kRow, c = q % kRow * kPer;
+            at[i] = KFAST ? x + min(line, own - 1) * ld + c : x + line * ld + min(c, own - 1);
+        }
+    }
+    // whether fetch() stays inside: k0 .. k0 + n - 1 are in the sum (of K
+    // terms), and where a chunk may pass a row's end another row follows
+    static LS_DEV bool inside(long long ld, int k0, int n, int K) {
+        return KFAST ? k0 + n <= K : k0 + n < K && ld >= kPer;
+    }
+    LS_DEV void fetch(u32x4 (&r)[kLoads], long long ld, int k0) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) r[i] = *reinterpret_cast<const Words*>(at[i] + (KFAST ? k0 : k0 * ld));
+    }
     // chunks of k0 .. of X (row i, k: x[i * ld + k], or x[k * ld + i]), zeros
     // past `own` rows and K
     static LS_DEV void get(u32x4 (&r)[kLoads], const T* __restrict__ x, long long ld, int own, int k0, int K, int tid) {
@@ -40,7 +62,6 @@ struct AnyOperand : StepLds<R, KFAST, PAIRED> {
             const int row = KFAST ? line : k0 + line, col = KFAST ? k0 + at : at;
             const int left = row < (KFAST ? own : K) ? (KFAST ? K : own) - col : 0;
             const T* p = x + row * ld + col;
-            typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));  // at any element
             if (left >= kPer) {
                 r[i] = *reinterpret_cast<const Words*>(p);
             } else {
@@ -72,6 +93,29 @@ LS_DEV void put_any(const Piece<T>& p, long long i, int j, float v) {
     p.c[i * p.ldc + j] = from_f<T>(act_of<ACT, T>(v));
 }
 
+// eight of a row's elements of 16 bits
+template <class T, int FORM, int ACT>
+LS_DEV void put_any8(const Piece<T>& p, long long i, int j, const float (&v)[8]) {
+    if (j + 8 > p.N) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (j + r < p.N) put_any<T, FORM, ACT>(p, i, j + r, v[r]);
+        return;
+    }
+    struct { T v[8]; } c, b = {};
+    struct { typename ZKeep<T>::type v[8]; } z;
+    if (FORM == kFormY && p.bias) b = __builtin_bit_cast(decltype(b), *reinterpret_cast<const Words*>(p.bias + j));
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const float x = FORM == kFormY ? v[r] + to_f(b.v[r]) : v[r];
+        if (FORM == kFormY && ACT != kActNone) z.v[r] = ZKeep<T>::template make<ACT>(x);
+        c.v[r] = from_f<T>(act_of<ACT, T>(x));
+    }
+    if (FORM == kFormY && ACT != kActNone && p.z)
+        *reinterpret_cast<Words*>(p.z + i * p.ldc + j) = __builtin_bit_cast(u32x4, z);
+    *reinterpret_cast<Words*>(p.c + i * p.ldc + j) = __builtin_bit_cast(u32x4, c);
+}
+
 // B x B of a piece from row i0 and column j0; SPLIT: the waves share the sum
 template <class T, int FORM, int ACT, int B, bool SPLIT>
 LS_DEV void any_tile(const Piece<T>& p, int i0, int j0, char* lds) {
@@ -101,7 +145,19 @@ LS_DEV void any_tile(const Piece<T>& p, int i0, int j0, char* lds) {
     using Acc = std::conditional_t<k16, f32x4, f32x16>;
     Acc acc[F][F] = {};
     u32x4 ra[kAnySteps][OpA::kLoads], rb[kAnySteps][OpB::kLoads];
+    OpA oa;
+    OpB ob;
+    oa.place(a, p.lda, M, tid);
+    ob.place(b, p.ldb, N, tid);
     auto get = [&](int k) {
+        if (k + kDeep <= K && OpA::inside(p.lda, k, kDeep, p.K) && OpB::inside(p.ldb, k, kDeep, p.K)) {
+#pragma unroll
+            for (int h = 0; h < kAnySteps; ++h) {
+                oa.fetch(ra[h], p.lda, k + h * kStepK);
+                ob.fetch(rb[h], p.ldb, k + h * kStepK);
+            }
+            return;
+        }
 #pragma unroll
         for (int h = 0; h < kAnySteps; ++h) {
             OpA::get(ra[h], a, p.lda, M, k + h * kStepK, K, tid);
@@ -156,9 +212,22 @@ LS_DEV void any_tile(const Piece<T>& p, int i0, int j0, char* lds) {
         }
         buf = kBuffer - buf;
     }
-    // where a lane's sums lie: 16-bit, row l % 16 of fragment i and columns
+    // Where a lane's sums lie: 16-bit, row l % 16 of fragment i and columns
     // 8 (l / 16) + 4 (j & 1) + r of the pair j / 2; fp32, rows
     // 8 (r / 4) + 4 (l / 32) + r % 4 and column l % 32
+    if constexpr (k16 && !SPLIT) {
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; j += 2) {
+                const int row = r0 + i * 16 + (l & 15), col = c0 + j * 16 + (l >> 4) * 8;
+                float v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
+                if (row < M) put_any8<T, FORM, ACT>(p, i0 + row, j0 + col, v);
+            }
+        return;
+    }
     auto each = [&](auto&& f) {
 #pragma unroll
         for (int i = 0; i < F; ++i)
