@@ -318,44 +318,57 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
 // A workgroup takes kDzRows rows of one expert and 64 V columns, a wave a
 // quarter of the rows; the waves' sums are added in wave order, one partial
 // row per tile of rows, and k_dbias adds an expert's partials in their order.
-template <class R>
-LS_DEV R once(const void* p) {
-    if constexpr (sizeof(R) == 16) {
-        typedef uint32_t Words __attribute__((ext_vector_type(4)));
-        return __builtin_bit_cast(R, __builtin_nontemporal_load(reinterpret_cast<const Words*>(p)));
-    } else {
-        return *reinterpret_cast<const R*>(p);
-    }
-}
-
+//
+// With V = 16 bytes a lane takes them at any element's address; where that
+// leaves fewer than two workgroups for a CU it takes one element of 16 rows
+// instead (16 bytes / one element, silu and the sums, us: 1026 rows of 1001 in
+// fp32 11.7 / 7.8, 4096 of 1024 in bf16 18.2 / 9.9, 8192 of 1024 20.5 / 16.5,
+// 16384 of 1024 25.2 / 24.1, 8192 of 2001 27.7 / 35.2, 32768 of 4095 164 /
+// 222).  Memory bounds it: 32768 rows of 4096 in bf16, 805 MB: 144 us.
 template <class T, int ACT, int V>
 LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const int32_t* __restrict__ off, int P,
-                    int E, int N, T* __restrict__ dz, float* __restrict__ part, int ti, int tj, float (*s)[64 * V]) {
+                    int E, int N, T* __restrict__ dz, float* __restrict__ part, int ti, int tj,
+                    float (*s)[64 * V]) {
     using Z = typename ZKeep<T>::type;
     const RowTile t = find_row_tile<kDzRows>(off, E, P, ti);
     if (t.lo >= t.hi || t.e >= E) return;
     const int l = lane_id(), w = threadIdx.x >> 6;
-    const long long c = (long long)tj * (64 * V) + l * V;
+    // the lane's columns; at a row's end the last V of the row, which other
+    // lanes have in part too: both write the same values
+    const bool on = (long long)tj * (64 * V) + l * V < N;
+    const long long c = min((long long)tj * (64 * V) + l * V, (long long)max(N - V, 0));
     float sum[V] = {};
-    // U rows' loads are in flight at a time (V = 1, 1026 rows of 1001: 12.4 us
-    // with 4, 11.5 with 16)
-    constexpr int U = V == 1 ? 16 : 4;
-    struct __attribute__((aligned(sizeof(T) * V))) PT {
+    constexpr int U = V == 1 ? 16 : 4;  // rows whose loads are in flight at a time
+    struct PT {
         T v[V];
     };
-    struct __attribute__((aligned(sizeof(Z) * V))) PZ {
+    struct __attribute__((packed, aligned(sizeof(T)))) Loose {  // at any element
+        PT p;
+    };
+    struct PZ {
         Z v[V];
     };
-    if (c < N) {
+    static_assert(V == 1 || (sizeof(PT) == 16 && sizeof(PZ) == 16));
+    // whole: rows have V columns and more
+    auto run = [&](auto whole) {
+        // what is read once goes past the caches, which dz is to fill
+        auto load = [&](auto& x, const auto* p) {
+            if constexpr (decltype(whole)::value) {
+                x = __builtin_bit_cast(std::decay_t<decltype(x)>,
+                                       __builtin_nontemporal_load(reinterpret_cast<const Words*>(p)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) x.v[i] = p[min(i, N - 1)];
+            }
+        };
         for (int r0 = t.lo + w; r0 < t.hi; r0 += 4 * U) {
             PT g[U];
             PZ z[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const long long at = (long long)min(r0 + 4 * u, t.hi - 1) * N + c;
-                // read once: past the caches, which dz is to fill
-                g[u] = once<PT>(dy + at);
-                if (ACT != kActNone) z[u] = once<PZ>((const Z*)zp + at);
+                load(g[u], dy + at);
+                if (ACT != kActNone) load(z[u], (const Z*)zp + at);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -373,18 +386,31 @@ LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const
                     }
                     sum[i] += d;
                 }
-                if (ACT != kActNone) *reinterpret_cast<PT*>(dz + (long long)r * N + c) = o;
+                if (ACT == kActNone) continue;
+                T* to = dz + (long long)r * N + c;
+                if constexpr (decltype(whole)::value) {
+                    reinterpret_cast<Loose*>(to)->p = o;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (i < N) to[i] = o.v[i];
+                }
             }
         }
+    };
+    if (on) {
+        if (V > 1 && N >= V) run(std::bool_constant<(V > 1)>{});
+        else run(std::false_type{});
     }
     if (!part) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) s[w][i * 64 + l] = sum[i];
     __syncthreads();
-    if (w != 0 || c >= N) return;
+    if (w != 0 || !on) return;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        part[(long long)ti * N + c + i] = (s[0][i * 64 + l] + s[1][i * 64 + l]) +
+        if (c + i < N)
+            part[(long long)ti * N + c + i] = (s[0][i * 64 + l] + s[1][i * 64 + l]) +
                                                   (s[2][i * 64 + l] + s[3][i * 64 + l]);
 }
 
@@ -431,16 +457,16 @@ void launch_expert_dz(const void* z, const void* dy, int dtype, int act, const i
         using T = decltype(tv);
         with_act(act, [&](auto av) {
             constexpr int A = decltype(av)::value;
+            auto launch = [&](auto vv) {
+                constexpr int V = decltype(vv)::value;
+                const int cols = (int)ceil_div(out, 64 * V);
+                const long long tiles = max_row_tiles<kDzRows>(P, E) * cols;
+                hipLaunchKernelGGL((k_dz<T, A, V>), dim3(grid_of(tiles)), dim3(256), 0, st, z, (const T*)dy, off, P,
+                                   E, out, (T*)dz, part, tiles, cols);
+            };
             constexpr int W = 16 / (int)sizeof(T);
-            const bool wide = out % W == 0 && aligned16(z) && aligned16(dy) && aligned16(dz);
-            const int cols = (int)ceil_div(out, wide ? 64 * W : 64);
-            const long long tiles = max_row_tiles<kDzRows>(P, E) * cols;
-            if (wide)
-                hipLaunchKernelGGL((k_dz<T, A, W>), dim3(grid_of(tiles)), dim3(256), 0, st, z, (const T*)dy, off, P, E,
-                                   out, (T*)dz, part, tiles, cols);
-            else
-                hipLaunchKernelGGL((k_dz<T, A, 1>), dim3(grid_of(tiles)), dim3(256), 0, st, z, (const T*)dy, off, P, E,
-                                   out, (T*)dz, part, tiles, cols);
+            if (max_row_tiles<kDzRows>(P, E) * ceil_div(out, 64 * W) >= 512) launch(std::integral_constant<int, W>{});
+            else launch(std::integral_constant<int, 1>{});
         });
     });
 }
