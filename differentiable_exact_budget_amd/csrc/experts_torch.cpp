@@ -3,7 +3,7 @@
 // module only marshals.  It is C++ because a small training step is bound by
 // the host: an autograd node written in Python runs in the engine's own thread
 // and takes the interpreter lock back and forth (dispatch with its gradient,
-// 1000 rows: 91 us, of which the GPU works 10).
+// 1000 rows: 91 us so, 46 us here, of which the GPU works 10).
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>

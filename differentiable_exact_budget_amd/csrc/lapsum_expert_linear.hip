@@ -11,6 +11,10 @@
 //    steps each, the next two steps' loads in flight while two are multiplied.
 //  - Few tiles: 32 x 32 a workgroup, and its four waves split the sum, each on
 //    its own in its own part of LDS; their results are added in wave order.
+// 32768 x 2047 rows -> 4095 in bf16: y 1.07 ms (0.51 PFLOP/s), dx 0.91 (0.59),
+// dW 0.82 (0.65), bound by the way through registers; 32768 x 2048 -> 4096 in
+// fp32: y 4.76 ms (116 TFLOP/s), dx 4.72, dW 4.41, the matrix instruction's
+// rate being 157.
 #include "lapsum_expert_tile.h"
 
 namespace lapsum {
@@ -303,11 +307,16 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
         launch_expert_mfma(form, dtype, g, st);
         return;
     }
-    // 128 x 128 tiles where they fill the CUs
+    // 128 x 128 tiles where there are enough of them, for 16-bit rows every
+    // second CU's, for fp32, whose tiles take eight times as long, more than
+    // one for each CU (128 / 32 wide, us, tiles counted as below: bf16 y, 95
+    // tiles 28.0 / 27.8, 120 tiles 29 / 29, 152 tiles 29 / 39, 280 tiles
+    // 36 / 63; fp32 y, 152 tiles 88 / 68, 280 tiles 145 / 118; fp32 dW, 512
+    // tiles 91 / 110, 896 tiles 59 / 77)
     const long long tiles = ceil_div(N, 128) * (form == kFormDw ? ceil_div(g.out, 128) * g.E : g.P / 128 + g.E / 2);
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
-        if (tiles >= 192) launch_any<T, 128, false>(form, g, st);
+        if (tiles >= (sizeof(T) == 2 ? 128 : 384)) launch_any<T, 128, false>(form, g, st);
         else launch_any<T, 32, true>(form, g, st);
     });
 }
@@ -324,7 +333,7 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
 // instead (16 bytes / one element, silu and the sums, us: 1026 rows of 1001 in
 // fp32 11.7 / 7.8, 4096 of 1024 in bf16 18.2 / 9.9, 8192 of 1024 20.5 / 16.5,
 // 16384 of 1024 25.2 / 24.1, 8192 of 2001 27.7 / 35.2, 32768 of 4095 164 /
-// 222).  Memory bounds it: 32768 rows of 4096 in bf16, 805 MB: 144 us.
+// 222).  Memory bounds it: 32768 rows of 4096 in bf16, 805 MB: 149 us.
 template <class T, int ACT, int V>
 LS_DEV void dz_tile(const void* __restrict__ zp, const T* __restrict__ dy, const int32_t* __restrict__ off, int P,
                     int E, int N, T* __restrict__ dz, float* __restrict__ part, int ti, int tj,
@@ -426,7 +435,8 @@ __global__ __launch_bounds__(256) void k_dz(const void* __restrict__ zp, const T
 }
 
 // An expert's partial sums, 64 columns a workgroup: a wave adds every fourth
-// tile's, eight loads in flight, and the waves' sums are added in wave order.
+// tile's, eight loads in flight, and the waves' sums are added in wave order
+// (4096 columns of 8 experts, 520 partial rows: 5.5 us).
 template <class T>
 __global__ __launch_bounds__(256) void k_dbias(const float* __restrict__ part, const int32_t* __restrict__ off, int P,
                                                int E, int N, T* __restrict__ dbias) {

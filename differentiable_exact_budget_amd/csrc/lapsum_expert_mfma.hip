@@ -23,6 +23,14 @@
 //  - Reads out of range return zero, which is all the masking that ragged
 //    experts need: a tile's buffer ends with its expert's last row.
 //
+// 32768 rows, 8 experts 2048 -> 4096 in bf16 (0.54 TFLOP): y 0.51 ms, 1.06
+// PFLOP/s; dx 0.48, dW 0.46.  What bounds it is the feed: the loads to LDS
+// alone, without a product, take 0.41 / 0.38 / 0.37 ms, a quarter of their
+// lines missing the L2; the matrix instructions alone would take 0.36.  A tile
+// costs about 10 us beside its products (its first loads and its epilogue),
+// which short sums feel: 16384 rows, 16 experts 1024 -> 4096 with gelu in f16
+// (0.14 TFLOP) take 0.20 ms.
+//
 // A wave's direct-to-LDS store is 64 consecutive chunks of the step's layout
 // in LDS, so the layout's permutation is made on the global side: each lane
 // fetches the chunk that belongs at its place.  B's fragments come in pairs

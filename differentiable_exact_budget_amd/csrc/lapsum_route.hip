@@ -199,7 +199,8 @@ void launch_expert_topk(const float* gates, long long T, int E, int m, float flo
 // A workgroup writes whole rows: `rows` rows of dgates are cleared in LDS,
 // every slot's value is put at its expert (the experts of a row differ), and
 // the rows go out as one contiguous run.  The row's sum of dw w is taken over
-// mp = the power of two >= m lanes.
+// mp = the power of two >= m lanes.  The stores bound it: 65536 rows of 257
+// gates, m = 8: 15.7 us for 74 MB, 4.7 TB/s, a large copy's rate.
 constexpr int kTopkVjpThreads = 256;
 constexpr int kTopkVjpFloats = 4096;
 

@@ -9,6 +9,10 @@
 // several 16-byte loads in flight (U stretches of 64 lanes), and with few
 // tokens a row is spread over many waves instead (U = 1).
 //
+// 16384 tokens of 2048 in bf16: dispatch to 2 slots 34 us and its gradient
+// 35 us for 201 MB each, 5.9 TB/s; combine of 4 slots with a residual 67 us for
+// 389 MB, 5.8 TB/s; its gradient 96 to 120 us for 590 MB, 4.9 to 6.1 TB/s.
+//
 // Rows need not start on 16 bytes: the hardware takes 16-byte loads and stores
 // at any element's address, and only a row's last elements go one by one.
 //
