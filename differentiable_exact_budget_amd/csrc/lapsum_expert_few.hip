@@ -4,9 +4,13 @@
 // A workgroup takes 16 rows of an expert and 16 of its outputs.  Its four
 // waves split the sum over k; each multiplies its quarter straight from memory
 // (a weight is used once, so LDS would only add a stop on its way): a fragment
-// is one 16-byte load a lane, eight steps of them in flight.  The waves' sums
-// meet in LDS and are added in wave order, with bias and activation behind.
-// Two rows, 2048 -> 4096 in bf16 (34 MB of weights): 15 us.
+// is one 16-byte load a lane, and with the few registers this takes (24) eight
+// waves of a SIMD have theirs in flight.  The waves' sums meet in LDS and are
+// added in wave order, with bias and activation behind.
+//
+// 64 rows at 41 of 64 experts 2048 -> 1024 in bf16, 172 MB of weights: 33 us
+// from memory, 5.2 TB/s, a large copy's rate, and 29 us from the memory-side
+// cache; with loads that pass the caches by, 36 us from either.
 #include "lapsum_expert_tile.h"
 
 namespace lapsum {
@@ -15,7 +19,7 @@ constexpr int kFewWaves = 4;
 
 template <class T, int ACT>
 __global__ __launch_bounds__(kFewWaves * 64) void k_product_few(LinearArgs g, int cols) {
-    constexpr int U = 8;  // steps of 32 k in flight
+    constexpr int U = 8;  // steps of 32 k without a masked end at a time
     using Z = typename ZKeep<T>::type;
     __shared__ float part[kFewWaves][16][20];
     const int l = lane_id(), w = uniform(threadIdx.x >> 6), i16 = l & 15, k8 = (l >> 4) * 8;
@@ -36,7 +40,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_product_few(LinearArgs g, in
             s16x8 fx[U], fb[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                fb[u] = __builtin_bit_cast(s16x8, __builtin_nontemporal_load((const u32x4*)(b + (s + u) * 32)));
+                fb[u] = *(const s16x8*)(b + (s + u) * 32);
                 fx[u] = *(const s16x8*)(x + (s + u) * 32);
             }
 #pragma unroll
@@ -63,8 +67,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_product_few(LinearArgs g, in
     if (ACT != kActNone && g.z && used) ((Z*)g.z)[to] = ZKeep<T>::template make<ACT>(v);
 }
 
+static long long few_tiles(const LinearArgs& g) { return max_row_tiles<16>(g.P, g.E) * ceil_div(g.out, 16); }
+
+// one tile a workgroup, whose threads a launch counts in 32 bits
+bool expert_few_takes(const LinearArgs& g) { return few_tiles(g) < (1ll << 32) / (kFewWaves * 64); }
+
 void launch_expert_few(int dtype, const LinearArgs& g, hipStream_t st) {
-    const long long cols = ceil_div(g.out, 16), tiles = max_row_tiles<16>(g.P, g.E) * cols;
+    const long long cols = ceil_div(g.out, 16), tiles = few_tiles(g);
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
         if constexpr (sizeof(T) == 2)

@@ -356,9 +356,14 @@ static int tile_side(int form, const LinearArgs& g) {
 }
 
 void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st) {
-    // so few rows that even 64-wide tiles leave most CUs without work: one
-    // token's two experts, 2048 -> 4096: 15 us, 18 us in tiles
-    if (form == kFormY && g.P * ceil_div(g.out, 64) < 256) {
+    // Few rows for each expert, or few at all: without LDS.  64-wide tiles / few,
+    // us, weights in the memory-side cache and from memory: 64 experts
+    // 2048 -> 1024, 1 row of an expert 27 / 29 and 44 / 33, 2 rows 35 / 36 and
+    // 57 / 42, 4 rows 38 / 43 and 64 / 51, 8 rows 40 / 51 and 65 / 62; 8 experts
+    // 2048 -> 4096, 2 rows 20 / 18 and 31 / 21; 64 experts 512 -> 1024, 4 rows
+    // 13 / 15 and 15 / 18; 16 experts 512 -> 512, 4 rows 5.7 / 4.1 and 6.8 / 4.4.
+    const bool few = (g.in >= 1024 && g.P <= 4 * g.E) || g.P * ceil_div(g.out, 64) < 1024;
+    if (form == kFormY && few && expert_few_takes(g)) {
         launch_expert_few(dtype, g, st);
         return;
     }

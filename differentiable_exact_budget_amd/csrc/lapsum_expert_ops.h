@@ -86,6 +86,7 @@ void launch_expert_product(int form, int dtype, const LinearArgs& g, hipStream_t
 bool expert_mfma_takes(int form, int dtype, const LinearArgs& g);
 void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st);
 // lapsum_expert_few.hip: kFormY with few rows an expert, for what expert_mfma_takes
+bool expert_few_takes(const LinearArgs& g);
 void launch_expert_few(int dtype, const LinearArgs& g, hipStream_t st);
 // dz (may be null: dz = dy, not written) and per-chunk column sums (may be
 // null) of dz; then the sums per expert
