@@ -279,6 +279,15 @@ def test_products_of_many_rows(dtype, T, m, E, K, F):
     check_product(dtype, T, m, E, K, F, "silu", idle=(2,), on="cuda")
 
 
+# many rows narrower than 16 bytes on one side or both, and up to four rows of
+# each expert over long sums with a masked end
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,m,E,K,F", [(20000, 2, 3, 5, 7), (20000, 2, 3, 3, 600), (20000, 2, 3, 600, 3),
+                                       (16, 4, 16, 1032, 200), (40, 2, 24, 1048, 40), (9, 4, 9, 2047, 33)])
+def test_products_of_narrow_rows_and_of_few_rows(dtype, T, m, E, K, F):
+    check_product(dtype, T, m, E, K, F, "silu", idle=(1,), on="cuda")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("act", ["relu", "gelu"])
 @pytest.mark.parametrize("T,m,E,K,F", [(50, 2, 4, 64, 128), (21, 3, 5, 33, 40), (300, 2, 3, 256, 264)])
