@@ -437,17 +437,24 @@ __global__ __launch_bounds__(256) void k_dz(const void* __restrict__ zp, const T
 // An expert's partial sums, 64 columns a workgroup: a wave adds every fourth
 // tile's, eight loads in flight, and the waves' sums are added in wave order
 // (4096 columns of 8 experts, 520 partial rows: 5.5 us).
+//
+// `tiles` rows of partial sums there are.  Offsets that a sort made need at
+// most so many; of offsets that run back, experts' rows overlap and would count
+// more, so an expert's first row and its number are held to them.
 template <class T>
 __global__ __launch_bounds__(256) void k_dbias(const float* __restrict__ part, const int32_t* __restrict__ off, int P,
-                                               int E, int N, T* __restrict__ dbias) {
+                                               int E, int N, int tiles, T* __restrict__ dbias) {
     __shared__ float s[4][64];
     const int e = blockIdx.y, l = lane_id(), w = uniform(threadIdx.x >> 6);
     // the expert's first tile of rows: those of the experts before it
     int first = 0;
     for (int i = l; i < e; i += 64)
         first += (max(row_at(off, i + 1, P) - row_at(off, i, P), 0) + kDzRows - 1) / kDzRows;
-    first = __builtin_amdgcn_readlane((int)wave_inclusive_scan((uint32_t)first), 63);
-    const int n = (max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + kDzRows - 1) / kDzRows;
+    // (a lane adds up at most 16 experts' tiles, below 2^29, and 64 lanes of at
+    // most `tiles` stay below 2^32)
+    const uint32_t before = wave_inclusive_scan((uint32_t)min(first, tiles));
+    first = (int)min((uint32_t)__builtin_amdgcn_readlane((int)before, 63), (uint32_t)tiles);
+    const int n = min((max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + kDzRows - 1) / kDzRows, tiles - first);
     const long long c = (long long)blockIdx.x * 64 + l;
     float sum = 0.0f;
     if (c < N) {
@@ -487,7 +494,7 @@ void launch_expert_dbias(const float* part, int dtype, const int32_t* off, int P
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
         hipLaunchKernelGGL(k_dbias<T>, dim3((unsigned)ceil_div(out, 64), (unsigned)E), dim3(256), 0, st, part, off, P,
-                           E, out, (T*)dbias);
+                           E, out, (int)max_row_tiles<kDzRows>(P, E), (T*)dbias);
     });
 }
 
