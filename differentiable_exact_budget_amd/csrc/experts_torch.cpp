@@ -195,6 +195,8 @@ void check_linear(const Tensor& xs, const Tensor& weight, const Plan& plan, cons
     check(weight, "weight", xs.scalar_type(), 3, &xs);
     check_shape(xs, "xs", {plan.pairs(), weight.size(2)});
     check_shape(weight, "weight", {plan.experts, weight.size(1), weight.size(2)});
+    TORCH_CHECK_VALUE(std::max(weight.size(1), weight.size(2)) <= LAPSUM_MAX_PAIRS, "weight must have at most ",
+                      LAPSUM_MAX_PAIRS, " rows and columns an expert (got ", weight.size(1), " x ", weight.size(2), ")");
     if (bias.defined()) {
         check(bias, "bias", xs.scalar_type(), 2, &xs);
         check_shape(bias, "bias", {plan.experts, weight.size(1)});

@@ -9,7 +9,9 @@ using namespace lapsum;
 
 namespace {
 
-constexpr int64_t kRowsMax = LAPSUM_MAX_PAIRS;  // row tiles' ends stay below 2^31
+// rows, and a product's widths: the ends of tiles and of a sum's steps stay
+// below 2^31
+constexpr int64_t kRowsMax = LAPSUM_MAX_PAIRS;
 constexpr int64_t kWidthMax = 0x7FFFFFFFll;
 
 hipStream_t stream_of(lapsum_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
@@ -22,6 +24,11 @@ bool good_tokens(int64_t tokens, int64_t slots) {
     return tokens >= 0 && slots >= 1 && slots <= LAPSUM_MAX_SLOTS && tokens <= kRowsMax / slots;
 }
 bool good_width(int64_t width) { return width >= 0 && width <= kWidthMax; }
+bool good_product(int64_t rows, int64_t in, int64_t out) {
+    for (const int64_t n : {rows, in, out})
+        if (n < 0 || n > kRowsMax) return false;
+    return true;
+}
 
 // dz of the 16-byte aligned scratch, then the bias gradient's partial sums
 struct VjpScratch {
@@ -126,7 +133,7 @@ lapsum_status_t lapsum_expert_combine_vjp(const void* ys, const float* weights, 
 lapsum_status_t lapsum_expert_linear(const void* xs, const void* weight, const void* bias, lapsum_dtype_t dtype,
                                      int64_t rows, int64_t in, int64_t out, int64_t experts, const int32_t* offsets,
                                      lapsum_act_t act, void* ys, void* z_out, lapsum_stream_t stream) {
-    if (!good_dtype(dtype) || !good_act(act) || rows < 0 || rows > kRowsMax || !good_width(in) || !good_width(out) ||
+    if (!good_dtype(dtype) || !good_act(act) || !good_product(rows, in, out) ||
         !good_experts(experts))
         return LAPSUM_ERR_INVALID_ARGUMENT;
     if (rows == 0 || out == 0) return LAPSUM_OK;
@@ -139,7 +146,7 @@ lapsum_status_t lapsum_expert_linear(const void* xs, const void* weight, const v
 
 size_t lapsum_expert_linear_vjp_scratch_bytes(lapsum_dtype_t dtype, int64_t rows, int64_t in, int64_t out,
                                               int64_t experts, lapsum_act_t act, int32_t want_dbias) {
-    if (!good_dtype(dtype) || !good_act(act) || rows < 0 || rows > kRowsMax || !good_width(in) || !good_width(out) ||
+    if (!good_dtype(dtype) || !good_act(act) || !good_product(rows, in, out) ||
         !good_experts(experts))
         return 0;
     return vjp_scratch(dtype, rows, out, experts, act, want_dbias != 0).bytes();
@@ -149,7 +156,7 @@ lapsum_status_t lapsum_expert_linear_vjp(const void* xs, const void* weight, con
                                          lapsum_dtype_t dtype, int64_t rows, int64_t in, int64_t out, int64_t experts,
                                          const int32_t* offsets, lapsum_act_t act, void* dxs, void* dweight,
                                          void* dbias, void* scratch, lapsum_stream_t stream) {
-    if (!good_dtype(dtype) || !good_act(act) || rows < 0 || rows > kRowsMax || !good_width(in) || !good_width(out) ||
+    if (!good_dtype(dtype) || !good_act(act) || !good_product(rows, in, out) ||
         !good_experts(experts) || (!dxs && !dweight && !dbias) || !offsets)
         return LAPSUM_ERR_INVALID_ARGUMENT;
     const bool work = rows > 0 && out > 0;

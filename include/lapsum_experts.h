@@ -58,7 +58,7 @@ typedef enum { LAPSUM_ACT_NONE = 0, LAPSUM_ACT_RELU = 1, LAPSUM_ACT_SILU = 2, LA
 
 #define LAPSUM_MAX_EXPERTS 1024 /* experts of a row, at most */
 #define LAPSUM_MAX_SLOTS 64     /* slots of a token, at most */
-#define LAPSUM_MAX_PAIRS 0x7FFF0000 /* tokens * slots, and rows of a product, at most */
+#define LAPSUM_MAX_PAIRS 0x7FFF0000 /* tokens * slots, and each side of a product, at most */
 
 /*
  * The m largest gates of every row.
@@ -139,7 +139,7 @@ lapsum_status_t lapsum_expert_combine_vjp(const void* ys, const float* weights, 
  *            wants it (not written past offsets[experts]).  z is kept in
  *            fp16 whatever the 16-bit type, infinite beyond its range: only
  *            the activation's slope is taken from it, which is 0 or 1 there.
- * rows <= LAPSUM_MAX_PAIRS, in and out < 2^31.
+ * rows, in and out <= LAPSUM_MAX_PAIRS.
  */
 lapsum_status_t lapsum_expert_linear(const void* xs, const void* weight, const void* bias, lapsum_dtype_t dtype,
                                      int64_t rows, int64_t in, int64_t out, int64_t experts, const int32_t* offsets,
