@@ -272,10 +272,10 @@ __global__ __launch_bounds__(kAnyThreads) void k_product_any(LinearArgs g, long 
         // tiles past the last (their number is only bounded here) have no rows
         Place<T> at;
         if constexpr (FORM == kFormDw) {
-            at = dw_place<T, B>(g, (int)t, cols);
+            at = dw_place<T, B>(g, t, cols);
         } else {
             RowTiles<B> rows(g.off, g.E, g.P);
-            at = row_place<T, FORM, B>(g, rows, (int)t, cols);
+            at = row_place<T, FORM, B>(g, rows, t, cols);
         }
         if (at.rows > 0 && at.q < at.rows * cols)
             any_tile<T, FORM, ACT, B, SPLIT>(at.p, at.q / cols * B, at.q % cols * B, lds);

@@ -101,11 +101,13 @@ struct Place {
 };
 
 // The piece of tile t of a row form, in tiles of BM rows and `cols` columns.
-template <class T, int FORM, int BM>
-LS_DEV Place<T> row_place(const LinearArgs& g, RowTiles<BM>& tiles, int t, int cols) {
+// I: int, or long long where a launch may count 2^31 tiles (their number is
+// only bounded, by one more for each expert; a piece has fewer).
+template <class T, int FORM, int BM, class I>
+LS_DEV Place<T> row_place(const LinearArgs& g, RowTiles<BM>& tiles, I t, int cols) {
     Place<T> r;
     Piece<T>& p = r.p;
-    const RowTile at = tiles.find(t / cols);
+    const RowTile at = tiles.find((int)(t / cols));
     const bool used = at.e < g.E;
     p.M = at.ehi - at.elo;
     p.N = FORM == kFormY ? g.out : g.in;
@@ -119,17 +121,17 @@ LS_DEV Place<T> row_place(const LinearArgs& g, RowTiles<BM>& tiles, int t, int c
     p.bias = FORM == kFormY && g.bias && used ? (const T*)g.bias + (long long)at.e * g.out : nullptr;
     p.z = FORM == kFormY && g.z && used ? (typename ZKeep<T>::type*)g.z + (long long)at.elo * p.N : nullptr;
     r.rows = (p.M + BM - 1) / BM;
-    r.q = t - at.first * cols;
+    r.q = (int)(t - (I)at.first * cols);
     return r;
 }
 // the same of the weight gradient
-template <class T, int BM>
-LS_DEV Place<T> dw_place(const LinearArgs& g, int t, int cols) {
+template <class T, int BM, class I>
+LS_DEV Place<T> dw_place(const LinearArgs& g, I t, int cols) {
     Place<T> r;
     Piece<T>& p = r.p;
     r.rows = (g.out + BM - 1) / BM;
-    const int e = t / (r.rows * cols);
-    r.q = t % (r.rows * cols);
+    const int e = (int)(t / (r.rows * cols));
+    r.q = (int)(t % (r.rows * cols));
     const int lo = uniform(row_at(g.off, e, g.P));
     p.M = g.out;
     p.N = g.in;

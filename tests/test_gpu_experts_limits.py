@@ -45,3 +45,24 @@ def test_gradients_of_overlapping_experts_stay_in_bounds(dtype, act):
     for e in range(E):
         value, tol = ref["db"] if e == 0 else part["db"] if e == 2 else [torch.zeros_like(t) for t in ref["db"]]
         R.check(db[e:e + 1], value, tol, f"db of expert {e}")
+
+
+WIDEST = 0x7FFF0000
+
+
+@pytest.mark.slow
+def test_more_tiles_than_32_bits_count():
+    """One row among 32 experts of the widest outputs: tiles are counted with
+    one more for each expert, 33 x 2^26 of 32 columns.  The sum is empty, so y
+    is the zeros that the product writes."""
+    E = 32
+    plan = L.expert_sort(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), E)
+    xs = torch.empty(1, 0, dtype=torch.bfloat16, device="cuda")
+    weight = torch.empty(E, WIDEST, 0, dtype=torch.bfloat16, device="cuda")
+    dirty = torch.full((1, WIDEST), math.nan, dtype=torch.bfloat16, device="cuda")
+    del dirty  # y gets this memory
+    y = L.expert_linear(xs, weight, plan)
+    assert y.shape == (1, WIDEST)
+    assert not y.any()
+    del y
+    torch.cuda.empty_cache()
