@@ -15,6 +15,8 @@
 // dW 0.82 (0.65), bound by the way through registers; 32768 x 2048 -> 4096 in
 // fp32: y 4.76 ms (116 TFLOP/s), dx 4.72, dW 4.41, the matrix instruction's
 // rate being 157.
+#include <algorithm>
+
 #include "lapsum_expert_tile.h"
 
 namespace lapsum {
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(256) void k_dz(const void* __restrict__ zp, const T
 // more, so an expert's first row and its number are held to them.
 template <class T>
 __global__ __launch_bounds__(256) void k_dbias(const float* __restrict__ part, const int32_t* __restrict__ off, int P,
-                                               int E, int N, int tiles, T* __restrict__ dbias) {
+                                               int E, int N, int tiles, long long c0, T* __restrict__ dbias) {
     __shared__ float s[4][64];
     const int e = blockIdx.y, l = lane_id(), w = uniform(threadIdx.x >> 6);
     // the expert's first tile of rows: those of the experts before it
@@ -455,7 +457,7 @@ __global__ __launch_bounds__(256) void k_dbias(const float* __restrict__ part, c
     const uint32_t before = wave_inclusive_scan((uint32_t)min(first, tiles));
     first = (int)min((uint32_t)__builtin_amdgcn_readlane((int)before, 63), (uint32_t)tiles);
     const int n = min((max(row_at(off, e + 1, P) - row_at(off, e, P), 0) + kDzRows - 1) / kDzRows, tiles - first);
-    const long long c = (long long)blockIdx.x * 64 + l;
+    const long long c = c0 + (long long)blockIdx.x * 64 + l;
     float sum = 0.0f;
     if (c < N) {
         const float* p = part + (long long)first * N + c;
@@ -493,8 +495,13 @@ void launch_expert_dbias(const float* part, int dtype, const int32_t* off, int P
     if (out < 1) return;
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
-        hipLaunchKernelGGL(k_dbias<T>, dim3((unsigned)ceil_div(out, 64), (unsigned)E), dim3(256), 0, st, part, off, P,
-                           E, out, (int)max_row_tiles<kDzRows>(P, E), (T*)dbias);
+        // one launch up to a grid's columns, 262144 of 1024 experts (walking
+        // on by the grid in the kernel: 0.2 us more for every call)
+        const long long most = kGridMax / E * 64;
+        for (long long c0 = 0; c0 < out; c0 += most)
+            hipLaunchKernelGGL(k_dbias<T>, dim3((unsigned)ceil_div(std::min(out - c0, most), 64), (unsigned)E),
+                               dim3(256), 0, st, part, off, P, E, out, (int)max_row_tiles<kDzRows>(P, E), c0,
+                               (T*)dbias);
     });
 }
 

@@ -66,3 +66,50 @@ def test_more_tiles_than_32_bits_count():
     assert not y.any()
     del y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.slow
+def test_products_of_the_widest_outputs():
+    """One row of one number to as many outputs as there may be, and back: each
+    result is one product of two bf16, rounded once."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    plan = L.expert_sort(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 1)
+    x = torch.full((1, 1), 1.5, dtype=torch.bfloat16, device="cuda")
+    weight, dys = (torch.empty(WIDEST, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    y = L.expert_linear(x, weight.view(1, -1, 1), plan)
+    assert torch.equal(y[0], weight * x[0])
+    del y
+    _, dw, db = L.expert_linear_vjp(x, weight.view(1, -1, 1), plan, None, dys.view(1, -1), want=(False, True, True))
+    assert torch.equal(dw.view(-1), dys * x[0])
+    assert torch.equal(db[0], dys)
+    del weight, dys, dw, db
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.slow
+def test_the_widest_rows_to_their_places_and_back():
+    D = 2 ** 31 - 1
+    g = torch.Generator(device="cuda").manual_seed(4)
+    plan = L.expert_sort(torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"), 2)
+    x = torch.empty(1, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    xs = L.expert_dispatch(x, plan)
+    assert torch.equal(xs[0], x[0]) and torch.equal(xs[1], x[0])
+    w = torch.tensor([[2.0, 0.5]], device="cuda")
+    out = L.expert_combine(xs, w, plan, residual=x)
+    assert torch.equal(out, x * 3.5)  # fp32 sums of multiples of x, exact
+    del out
+    # slot 0 is expert 1's row, behind expert 0's
+    dys, _ = L.expert_combine_vjp(xs, w, plan, x, want=(True, False))
+    assert torch.equal(dys[1], 2 * x[0]) and torch.equal(dys[0], 0.5 * x[0])
+    del dys
+    assert torch.equal(L.expert_dispatch_vjp(xs, plan), 2 * x)
+    # dw: marks at a row's ends and middle, so that the sum is exact
+    xs.zero_()
+    at = torch.tensor([0, 1, D // 2, D - 2, D - 1], device="cuda")
+    xs[0, at] = 1.0
+    xs[1, at] = 2.0
+    x.fill_(1.0)
+    _, dw = L.expert_combine_vjp(xs, w, plan, x, want=(False, True))
+    assert torch.equal(dw, torch.tensor([[10.0, 5.0]], device="cuda"))
+    del x, xs
+    torch.cuda.empty_cache()
