@@ -113,3 +113,42 @@ def test_the_widest_rows_to_their_places_and_back():
     assert torch.equal(dw, torch.tensor([[10.0, 5.0]], device="cuda"))
     del x, xs
     torch.cuda.empty_cache()
+
+
+def small_layer(dtype=torch.float32):
+    """{operator: (call, its tensors that have a gradient)}"""
+    g = gen(11)
+    T, m, E, K, F = 6, 2, 4, 16, 24
+    p = torch.rand(T, E, generator=g).cuda()
+    plan = L.expert_sort(L.expert_topk(p, m)[0], E)
+    x, xs, ys, res = (torch.randn(n, k, generator=g).to(dtype).cuda() for n, k in ((T, K), (T * m, K), (T * m, F), (T, F)))
+    weight, bias = torch.randn(E, F, K, generator=g).to(dtype).cuda(), torch.randn(E, F, generator=g).to(dtype).cuda()
+    w = torch.rand(T, m, generator=g).cuda()
+    return {
+        "expert_topk": (lambda p: L.expert_topk(p, m, normalize=True)[1], (p,)),
+        "expert_dispatch": (lambda x: L.expert_dispatch(x, plan), (x,)),
+        "expert_linear": (lambda xs, weight, bias: L.expert_linear(xs, weight, plan, bias=bias, activation="silu"),
+                          (xs, weight, bias)),
+        "expert_combine": (lambda ys, w, res: L.expert_combine(ys, w, plan, residual=res), (ys, w, res)),
+    }
+
+
+OPERATORS = ["expert_topk", "expert_dispatch", "expert_linear", "expert_combine"]
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_forward_mode_derivatives_are_refused(name, requires_grad):
+    """A tangent that an operator cannot carry on is not dropped: the call is refused, for each of its inputs."""
+    fw = torch.autograd.forward_ad
+    call, inputs = small_layer()[name]
+    inputs = [t.detach().requires_grad_(requires_grad) for t in inputs]
+    want = call(*inputs).detach()
+    with fw.dual_level():
+        for i in range(len(inputs)):
+            dual = [fw.make_dual(t, torch.ones_like(t)) if i == j else t for j, t in enumerate(inputs)]
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call(*dual)
+            with torch.no_grad(), pytest.raises(RuntimeError, match="forward-mode"):
+                call(*dual)
+        assert torch.equal(call(*inputs), want)  # without tangents as ever
