@@ -4,6 +4,7 @@
 // the host: an autograd node written in Python runs in the engine's own thread
 // and takes the interpreter lock back and forth (dispatch with its gradient,
 // 1000 rows: 91 us so, 46 us here, of which the GPU works 10).
+#include <ATen/TracerMode.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -98,7 +99,10 @@ struct On {
     lapsum_stream_t stream;
     explicit On(const Tensor& x)
         : guard(x.device()),
-          stream(reinterpret_cast<lapsum_stream_t>(c10::hip::getCurrentHIPStream(x.device().index()).stream())) {}
+          stream(reinterpret_cast<lapsum_stream_t>(c10::hip::getCurrentHIPStream(x.device().index()).stream())) {
+        // a trace would keep the outputs' allocation and none of the work
+        TORCH_CHECK(!at::tracer::impl::is_dispatch_enabled(), "the expert operators cannot be traced (torch.jit.trace)");
+    }
 };
 
 // A plan's arrays as they travel through autograd.

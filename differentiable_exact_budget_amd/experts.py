@@ -8,8 +8,8 @@
     out = expert_combine(ys, w, plan, residual=x)     # weighted rows back
 
 All of them but the sort are differentiable, once and in reverse mode (second
-derivatives and forward-mode tangents are refused); each gradient also has an
-entry point of its own (expert_*_vjp).  They run in liblapsum.so (hand-written HIP
+derivatives and forward-mode tangents are refused, and so is torch.jit.trace);
+each gradient also has an entry point of its own (expert_*_vjp).  They run in liblapsum.so (hand-written HIP
 for gfx950, the C ABI of include/lapsum_experts.h) on the caller's current
 stream, never wait for the device and can be captured into a graph: the number
 of pairs in use stays on the device, and every array that goes by positions

@@ -152,3 +152,13 @@ def test_forward_mode_derivatives_are_refused(name, requires_grad):
             with torch.no_grad(), pytest.raises(RuntimeError, match="forward-mode"):
                 call(*dual)
         assert torch.equal(call(*inputs), want)  # without tangents as ever
+
+
+@pytest.mark.parametrize("name", OPERATORS + ["expert_sort"])
+def test_traces_are_refused(name):
+    """A trace would record the outputs' allocation and none of the work."""
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    call, inputs = small_layer()[name] if name != "expert_sort" else (lambda ids: L.expert_sort(ids, 3).order, (ids,))
+    for grad in (False, True) if name != "expert_sort" else (False,):
+        with pytest.raises(RuntimeError, match="traced"):
+            torch.jit.trace(call, tuple(t.detach().requires_grad_(grad) for t in inputs), check_trace=False)
