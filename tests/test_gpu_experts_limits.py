@@ -162,3 +162,18 @@ def test_traces_are_refused(name):
     for grad in (False, True) if name != "expert_sort" else (False,):
         with pytest.raises(RuntimeError, match="traced"):
             torch.jit.trace(call, tuple(t.detach().requires_grad_(grad) for t in inputs), check_trace=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gelu_keeps_its_relative_accuracy_far_below_zero(dtype):
+    """For 16-bit rows gelu(z) = z Q(-z) with a polynomial Q that is 2.1e-4 Q
+    off at most; its exponential's argument, below 122 here, is rounded twice
+    (3e-5).  Then one rounding to the rows' type."""
+    z = torch.cat([torch.linspace(-13, -4, 4096), torch.linspace(-4, 4, 4096), torch.linspace(4, 13, 64)]).to(dtype)
+    F = z.numel()
+    plan = L.expert_sort(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 1)
+    y = L.expert_linear(torch.zeros(1, 16, dtype=dtype).cuda(), torch.zeros(1, F, 16, dtype=dtype).cuda(), plan,
+                        bias=z[None].cuda(), activation="gelu")
+    z = z.double()
+    ref = 0.5 * z * torch.special.erfc(-z / math.sqrt(2))
+    R.check(y[0], ref, R.rounded(ref, dtype, 2.4e-4 * ref.abs()), "gelu")
