@@ -231,30 +231,30 @@ std::tuple<Tensor, Tensor> linear_call(const Tensor& xs, const Tensor& weight, c
     return {ys, z};
 }
 
+// xs is read for dweight only, weight for dxs only: where those are not wanted
+// either may be missing.
 std::tuple<Tensor, Tensor, Tensor> linear_vjp_call(const Tensor& xs, const Tensor& weight, const Plan& plan,
                                                    const Tensor& z, const Tensor& dys, int act,
                                                    std::array<bool, 3> want) {
-    check_linear(xs, weight, plan, Tensor());
-    const int64_t rows = xs.size(0), in = xs.size(1), out = weight.size(1);
-    check(dys, "dys", xs.scalar_type(), 2, &xs);
-    check_shape(dys, "dys", {rows, out});
+    const int64_t rows = dys.size(0), out = dys.size(1),
+                  in = xs.defined() ? xs.size(1) : weight.defined() ? weight.size(2) : 0;
     if (act != LAPSUM_ACT_NONE) {
         TORCH_CHECK_VALUE(z.defined(), "z is needed with an activation");
-        check(z, "z", z_type(xs), 2, &xs);
+        check(z, "z", z_type(dys), 2, &dys);
         check_shape(z, "z", {rows, out});
     }
-    const On on(xs);
+    const On on(dys);
     Tensor dxs, dweight, dbias, scratch;
-    if (want[0]) dxs = at::empty(xs.sizes(), xs.options());
-    if (want[1]) dweight = at::empty(weight.sizes(), xs.options());
-    if (want[2]) dbias = at::empty({plan.experts, out}, xs.options());
+    if (want[0]) dxs = at::empty({rows, in}, dys.options());
+    if (want[1]) dweight = at::empty({plan.experts, out, in}, dys.options());
+    if (want[2]) dbias = at::empty({plan.experts, out}, dys.options());
     int64_t elements = 0;
     for (const Tensor* t : {&dxs, &dweight, &dbias}) elements += t->defined() ? t->numel() : 0;
     if (elements == 0) return {dxs, dweight, dbias};
-    const auto dt = type_of(xs);
+    const auto dt = type_of(dys);
     if (const size_t n = lapsum_expert_linear_vjp_scratch_bytes(dt, rows, in, out, plan.experts, (lapsum_act_t)act,
                                                                 want[2]))
-        scratch = at::empty({(int64_t)n}, xs.options().dtype(at::kByte));
+        scratch = at::empty({(int64_t)n}, dys.options().dtype(at::kByte));
     check_ok(lapsum_expert_linear_vjp(ptr<void>(xs), ptr<void>(weight), ptr<void>(z), ptr<void>(dys), dt, rows, in, out,
                                       plan.experts, plan.off(), (lapsum_act_t)act, ptr<void>(dxs), ptr<void>(dweight),
                                       ptr<void>(dbias), ptr<void>(scratch), on.stream),
@@ -283,18 +283,17 @@ Tensor combine_call(const Tensor& ys, const Tensor& w, const Tensor& residual, c
     return out;
 }
 
+// ys is read for dw only: where that is not wanted it may be missing.
 std::tuple<Tensor, Tensor> combine_vjp_call(const Tensor& ys, const Tensor& w, const Plan& plan, const Tensor& dout,
                                             std::array<bool, 2> want) {
-    check_combine(ys, w, plan);
-    check(dout, "dout", ys.scalar_type(), 2, &ys);
-    check_shape(dout, "dout", {plan.tokens(), ys.size(1)});
-    const On on(ys);
+    const On on(dout);
+    const int64_t width = dout.size(1);
     Tensor dys, dw;
-    if (want[0]) dys = at::empty(ys.sizes(), ys.options());
+    if (want[0]) dys = at::empty({plan.pairs(), width}, dout.options());
     if (want[1]) dw = at::empty(w.sizes(), w.options());
     if ((dys.defined() ? dys.numel() : 0) + (dw.defined() ? dw.numel() : 0) == 0) return {dys, dw};
-    check_ok(lapsum_expert_combine_vjp(ptr<void>(ys), ptr<float>(w), ptr<void>(dout), type_of(ys), plan.tokens(),
-                                       plan.slots(), ys.size(1), plan.experts, plan.off(), plan.at(), ptr<void>(dys),
+    check_ok(lapsum_expert_combine_vjp(ptr<void>(ys), ptr<float>(w), ptr<void>(dout), type_of(dout), plan.tokens(),
+                                       plan.slots(), width, plan.experts, plan.off(), plan.at(), ptr<void>(dys),
                                        ptr<float>(dw), on.stream),
              "lapsum_expert_combine_vjp");
     return {dys, dw};
@@ -351,7 +350,8 @@ struct Linear : torch::autograd::Function<Linear> {
         const Tensor xs = xs_.contiguous(), weight = weight_.contiguous(), bias = bias_.value_or(Tensor());
         auto [ys, z] = linear_call(xs, weight, bias.defined() ? bias.contiguous() : bias, {experts, offsets, place},
                                    (int)act, true);
-        ctx->save_for_backward({xs, weight, z, offsets, place});
+        // what the gradients that are wanted read, and no more
+        ctx->save_for_backward({recorded(weight_) ? xs : Tensor(), recorded(xs_) ? weight : Tensor(), z, offsets, place});
         ctx->saved_data["experts"] = experts;
         ctx->saved_data["act"] = act;
         return ys;
@@ -372,7 +372,7 @@ struct Combine : torch::autograd::Function<Combine> {
                           const Tensor& place) {
         at::AutoDispatchBelowADInplaceOrView below;
         const Tensor ys = ys_.contiguous(), w = w_.contiguous(), residual = residual_.value_or(Tensor());
-        ctx->save_for_backward({ys, w, offsets, place});
+        ctx->save_for_backward({recorded(w_) ? ys : Tensor(), w, offsets, place});
         ctx->saved_data["experts"] = experts;
         return combine_call(ys, w, residual.defined() ? residual.contiguous() : residual, {experts, offsets, place});
     }
@@ -435,8 +435,11 @@ std::tuple<std::optional<Tensor>, std::optional<Tensor>, std::optional<Tensor>> 
     const Tensor& xs, const Tensor& weight, const std::optional<Tensor>& z, const Tensor& dys,
     const std::string& activation, std::array<bool, 3> want, int64_t experts, const Tensor& offsets,
     const Tensor& order, const Tensor& place) {
-    auto [a, b, c] = linear_vjp_call(xs, weight, make_plan(experts, offsets, order, place, xs), z.value_or(Tensor()),
-                                     dys, act_of(activation), want);
+    const Plan plan = make_plan(experts, offsets, order, place, xs);
+    check_linear(xs, weight, plan, Tensor());
+    check(dys, "dys", xs.scalar_type(), 2, &xs);
+    check_shape(dys, "dys", {xs.size(0), weight.size(1)});
+    auto [a, b, c] = linear_vjp_call(xs, weight, plan, z.value_or(Tensor()), dys, act_of(activation), want);
     return {maybe(a), maybe(b), maybe(c)};
 }
 
@@ -453,7 +456,11 @@ std::tuple<std::optional<Tensor>, std::optional<Tensor>> combine_vjp(const Tenso
                                                                      const Tensor& dout, std::array<bool, 2> want,
                                                                      int64_t experts, const Tensor& offsets,
                                                                      const Tensor& order, const Tensor& place) {
-    auto [a, b] = combine_vjp_call(ys, w, make_plan(experts, offsets, order, place, ys), dout, want);
+    const Plan plan = make_plan(experts, offsets, order, place, ys);
+    check_combine(ys, w, plan);
+    check(dout, "dout", ys.scalar_type(), 2, &ys);
+    check_shape(dout, "dout", {plan.tokens(), ys.size(1)});
+    auto [a, b] = combine_vjp_call(ys, w, plan, dout, want);
     return {maybe(a), maybe(b)};
 }
 

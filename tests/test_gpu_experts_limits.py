@@ -177,3 +177,25 @@ def test_gelu_keeps_its_relative_accuracy_far_below_zero(dtype):
     z = z.double()
     ref = 0.5 * z * torch.special.erfc(-z / math.sqrt(2))
     R.check(y[0], ref, R.rounded(ref, dtype, 2.4e-4 * ref.abs()), "gelu")
+
+
+@pytest.mark.parametrize("name", ["expert_linear", "expert_combine"])
+def test_only_what_the_wanted_gradients_read_is_kept(name):
+    """dxs reads the weights, dweight the rows, the combined rows' gradient the
+    gates and the gates' gradient the rows: what no wanted gradient reads is
+    not kept between the passes, and the gradients are as with all wanted."""
+    call, inputs = small_layer()[name]
+    dout = torch.randn(call(*inputs).shape, generator=gen(5)).cuda()
+    leaves = [t.detach().requires_grad_(True) for t in inputs]
+    all_grads = torch.autograd.grad(call(*leaves), leaves, dout)
+    readers = {"expert_linear": ((1,), (0,), ()), "expert_combine": ((), (0,), ())}[name]  # rows and weights
+    for i in range(3):
+        leaves = [t.detach().requires_grad_(i == j) for j, t in enumerate(inputs)]
+        kept = []
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: (kept.append(t.data_ptr()), t)[1], lambda t: t):
+            out = call(*leaves)
+        for j in range(3):
+            if j == 1 and name == "expert_combine":
+                continue  # the gates, a number for every row
+            assert (inputs[j].data_ptr() in kept) == (j in readers[i]), (i, j)
+        assert torch.equal(torch.autograd.grad(out, leaves[i], dout)[0], all_grads[i])
