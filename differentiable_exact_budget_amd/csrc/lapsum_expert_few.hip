@@ -9,7 +9,7 @@
 // added in wave order, with bias and activation behind.
 //
 // 64 rows at 41 of 64 experts 2048 -> 1024 in bf16, 172 MB of weights: 33 us
-// from memory, 5.2 TB/s, a large copy's rate, and 29 us from the memory-side
+// from memory, 5.2 TB/s (a large copy moves 4.9), and 29 us from the memory-side
 // cache; with loads that pass the caches by, 36 us from either.
 #include "lapsum_expert_tile.h"
 

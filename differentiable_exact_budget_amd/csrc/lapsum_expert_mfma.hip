@@ -23,13 +23,16 @@
 //  - Reads out of range return zero, which is all the masking that ragged
 //    experts need: a tile's buffer ends with its expert's last row.
 //
-// 32768 rows, 8 experts 2048 -> 4096 in bf16 (0.54 TFLOP): y 0.51 ms, 1.06
-// PFLOP/s; dx 0.48, dW 0.46.  What bounds it is the feed: the loads to LDS
-// alone, without a product, take 0.41 / 0.38 / 0.37 ms, a quarter of their
-// lines missing the L2; the matrix instructions alone would take 0.36.  A tile
-// costs about 10 us beside its products (its first loads and its epilogue),
-// which short sums feel: 16384 rows, 16 experts 1024 -> 4096 with gelu in f16
-// (0.14 TFLOP) take 0.20 ms.
+// 32768 rows, 8 experts 2048 -> 4096 in bf16 (0.55 TFLOP): y 0.50 ms, 1.1
+// PFLOP/s; dx 0.47, dW 0.44.  What bounds it is the feed: the loads to LDS
+// alone, without a product, take 0.41 / 0.38 / 0.37 ms; the matrix instructions
+// alone would take 0.36.  By the counters the matrix pipes work 44 / 54 / 51 %
+// of the time (y with silu, dx, dW) and 32 / 25 / 21 % of the requests miss the
+// L2.  A tile's first loads and its epilogue stand alone, no products beside
+// them: an activation adds what its instructions take (silu 16 us to y's 500,
+// gelu 46), and short sums feel it most: 16384 rows, 16 experts 1024 -> 4096 in
+// f16 (0.14 TFLOP, 96 us at a large product's rate) take 160 us without one,
+// 169 with silu, 189 with gelu.
 //
 // A wave's direct-to-LDS store is 64 consecutive chunks of the step's layout
 // in LDS, so the layout's permutation is made on the global side: each lane
@@ -344,6 +347,10 @@ bool expert_mfma_takes(int form, int dtype, const LinearArgs& g) {
 //   dW, 8 experts, 512 x 512, 32 tiles:     17 / 21 / 21
 //       8 experts, 2048 x 1024, 256 tiles:  21 / 19 / 18
 //       64 experts, 1024 x 2048, R = 1:     79 / 65 / 73
+// R takes the experts without rows in, so rows that are all one expert's among
+// many get too small a tile: 4096 rows 1024 -> 128, y 58 us as one of 1024
+// experts and 8 as the only one.  And dW's sum is never split over workgroups:
+// 65536 rows of 4 experts 64 -> 64 take 83 us on 4 of them, their bytes 3.
 static int tile_side(int form, const LinearArgs& g) {
     const long long per = g.P / g.E;
     if (form == kFormDw) {

@@ -1,8 +1,11 @@
 // What the experts' matrix kernels share: the 16-bit matrix instruction and
 // how a step's operand lies in LDS (gfx950).
 //
-// A step is 64 bytes of k of R rows.  Free of bank conflicts for the reads
-// below (the hardware serves 128 bytes of LDS at a time):
+// A step is 64 bytes of k of R rows, laid out against bank conflicts in the
+// reads below (the hardware serves 128 bytes of LDS at a time).  The counters of
+// the 256-wide tiles show none where k is contiguous in both operands, and
+// conflicts in a third of the cycles that LDS indexes with one transposed
+// operand, in half of them with two:
 //   k contiguous: row i has 4 chunks of 16 bytes, two rows to a line of 128;
 //     chunk c lies at c ^ fold(line) within its row's half.  A fragment is one
 //     16-byte read a lane.
