@@ -15,12 +15,18 @@ from ._binding import (PATH_AUTO, PATH_BRACKET, PATH_FORCE_FALLBACK, PATH_FULL, 
                        default_options, lib)
 from .experts import (ExpertPlan, expert_combine, expert_combine_vjp, expert_dispatch, expert_dispatch_vjp,
                       expert_linear, expert_linear_forward, expert_linear_vjp, expert_sort, expert_topk, expert_topk_vjp)
+from .experts8 import ScaledRows, expert_dequantize, expert_linear_fp8, expert_quantize
+from .layers import (layer_norm, layer_norm_forward, layer_norm_vjp, linear_cross_entropy,
+                     linear_cross_entropy_forward, linear_cross_entropy_vjp)
 
 __all__ = ["forward", "vjp", "vjp_kt", "soft_topk", "topk_threshold", "hard_topk", "dftopk",
            "forward_rows", "vjp_rows", "soft_topk_rows", "SoftTopK", "default_options", "Options", "Stats", "LapsumError",
            "PATH_AUTO", "PATH_FULL", "PATH_BRACKET", "PATH_FORCE_FALLBACK", "release_workspaces",
            "ExpertPlan", "expert_topk", "expert_topk_vjp", "expert_sort", "expert_dispatch", "expert_dispatch_vjp",
-           "expert_linear", "expert_linear_forward", "expert_linear_vjp", "expert_combine", "expert_combine_vjp"]
+           "expert_linear", "expert_linear_forward", "expert_linear_vjp", "expert_combine", "expert_combine_vjp",
+           "ScaledRows", "expert_quantize", "expert_dequantize", "expert_linear_fp8",
+           "layer_norm", "layer_norm_forward", "layer_norm_vjp",
+           "linear_cross_entropy", "linear_cross_entropy_forward", "linear_cross_entropy_vjp"]
 
 
 def _check_scores(x: torch.Tensor, name: str) -> None:

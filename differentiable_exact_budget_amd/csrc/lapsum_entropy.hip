@@ -1,0 +1,448 @@
+// Softmax cross entropy of a product with a vocabulary's weights: the steps
+// around the products, and the products of every type, size and alignment.
+//
+// Mathematics: z = x W^T + b, lse = log sum over v of e^z_v, loss = lse -
+// z_target; with g the loss' gradient, d = (e^(z - lse) - onehot) g and
+//   dx = d W,  dW = d^T x,  db = sum of d over the rows.
+//
+// z is never kept whole.  Forward, columns are taken in parts: each leaves a
+// row's maximum and its sum of exponentials about it, which launch_loss_rows
+// merges.  Backward, z is formed again, a piece of the vocabulary at a time,
+// and turned into d by the lse of the forward pass.
+//
+// Here pieces of z are formed in fp32 in scratch by the products for any
+// alignment (lapsum_tile_any.h) and read from there.  d is rounded to the rows'
+// type once, because the matrix instructions take it so; for fp16, whose range
+// ends at 6e-8, d is scaled by a power of two that brings the largest gradient
+// of a row's loss to 2^13 .. 2^14, and the products are scaled back in fp32.
+#include "lapsum_layer_ops.h"
+#include "lapsum_tile_any.h"
+
+namespace lapsum {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr long long kPieceBytes = 128ll << 20;  // of fp32 logits
+static_assert(sizeof(float2) == 8);
+
+static size_t take(size_t& at, size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return here;
+}
+
+static int any_width(const LossArgs& g) {
+    const long long w = std::max(kPieceBytes / 4 / std::max(g.T, 1) / 128 * 128, 128ll);
+    return (int)std::min<long long>(w, std::max(g.V, 1));
+}
+
+LossParts loss_any_parts(const LossArgs& g) {
+    LossParts p{};
+    p.width = any_width(g);
+    p.parts = (int)ceil_div(g.V, p.width);
+    size_t at = 0;
+    p.pairs = take(at, (size_t)p.parts * g.T * sizeof(float2));
+    p.zt = take(at, (size_t)g.T * 4);
+    p.loss = take(at, (size_t)g.T * 4);
+    p.logits = take(at, (size_t)g.T * p.width * 4);
+    p.bytes = at;
+    return p;
+}
+
+// dx's sum over a piece is shared out where its tiles are few
+static int any_shares(const LossArgs& g, int width) {
+    const long long tiles = ceil_div(g.T, 32) * ceil_div(g.D, 32);
+    return (int)std::max(1ll, std::min<long long>(512 / std::max(tiles, 1ll), width / 512));
+}
+
+LossVjpPlan loss_any_plan(int dtype, const LossArgs& g) {
+    LossVjpPlan p{};
+    p.width = any_width(g);
+    p.ld = p.width;
+    p.pieces = (int)ceil_div(g.V, p.width);
+    p.shares = any_shares(g, p.width);
+    size_t at = 0;
+    p.g = take(at, ((size_t)g.T + 1) * 4);
+    p.logits = take(at, (size_t)g.T * p.width * 4);
+    // fp32: in the logits' place
+    p.d = dtype == kF32 ? p.logits : take(at, (size_t)g.T * p.width * dtype_size(dtype));
+    if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
+    p.bytes = at;
+    return p;
+}
+
+// ---- the products ---------------------------------------------------------------
+
+template <class T>
+struct PutLogits {
+    float* c;
+    const T* bias;
+    long long ldc;
+    LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = bias ? v + to_f(bias[j]) : v; }
+};
+struct PutPart {
+    float* c;
+    long long ldc;
+    bool add;
+    LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = add ? c[i * ldc + j] + v : v; }
+};
+template <class T>
+struct PutOut {
+    T* c;
+    long long ldc;
+    float unscale;
+    LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = from_f<T>(v * unscale); }
+};
+// (eight at a time, one by one)
+template <class P>
+struct Each : P {
+    int N;
+    LS_DEV void eight(int i, int j, const float (&v)[8]) const {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (j + r < N) P::one(i, j + r, v[r]);
+    }
+};
+
+struct AnyProduct {
+    const void *a, *b;
+    int M, N, K, lda, ldb;
+    void* c;
+    long long ldc;
+    const void* bias;      // kFormY
+    const float* unscale;  // outputs
+    int shares;            // of K: partial sums, M * N elements apart
+    bool add;
+};
+// FORM kFormY: fp32 logits; kFormDx: partial sums (PART) or rows; kFormDw: rows
+template <class T, int FORM, bool PART, int B, bool SPLIT>
+__global__ __launch_bounds__(kAnyThreads) void k_loss_any(AnyProduct g, long long tiles, int cols) {
+    constexpr bool kA = FORM != kFormDw, kB = FORM == kFormY;
+    __shared__ __align__(128) char lds[2 * any_steps(SPLIT) * 2 * B * 64 * (SPLIT ? 4 : 1)];
+    for (long long t = blockIdx.x; t < tiles * g.shares; t += gridDim.x) {
+        const int share = (int)(t / tiles);
+        const long long q = t % tiles;
+        const int i0 = (int)(q / cols) * B, j0 = (int)(q % cols) * B;
+        const int k0 = (int)((long long)g.K * share / g.shares), k1 = (int)((long long)g.K * (share + 1) / g.shares);
+        const T* a = (const T*)g.a + (kA ? (long long)i0 * g.lda + k0 : (long long)k0 * g.lda + i0);
+        const T* b = (const T*)g.b + (kB ? (long long)j0 * g.ldb + k0 : (long long)k0 * g.ldb + j0);
+        auto sums = [&](const auto& put) {
+            any_sums<T, kA, kB, B, SPLIT>(a, g.M - i0, g.lda, b, g.N - j0, g.ldb, k1 - k0, lds, put);
+        };
+        const long long to = (long long)i0 * g.ldc + j0;
+        if constexpr (FORM == kFormY) {
+            Each<PutLogits<T>> put{{(float*)g.c + to, g.bias ? (const T*)g.bias + j0 : nullptr, g.ldc}, g.N - j0};
+            sums(put);
+        } else if constexpr (PART) {
+            Each<PutPart> put{{(float*)g.c + (long long)share * g.M * g.ldc + to, g.ldc, g.add}, g.N - j0};
+            sums(put);
+        } else {
+            Each<PutOut<T>> put{{(T*)g.c + to, g.ldc, *g.unscale}, g.N - j0};
+            sums(put);
+        }
+        __syncthreads();
+    }
+}
+
+template <int FORM, bool PART>
+static void launch_any_product(int dtype, const AnyProduct& g, hipStream_t st) {
+    if (g.M < 1 || g.N < 1) return;
+    with_dtype(dtype, [&](auto tv) {
+        using T = decltype(tv);
+        auto launch = [&](auto bv, auto sv) {
+            constexpr int B = bv.value;
+            const long long cols = ceil_div(g.N, B), tiles = cols * ceil_div(g.M, B);
+            hipLaunchKernelGGL((k_loss_any<T, FORM, PART, B, sv.value>), dim3(grid_of(tiles * g.shares)),
+                               dim3(kAnyThreads), 0, st, g, tiles, (int)cols);
+        };
+        // as for the experts' products: wide tiles where there are enough
+        const long long tiles = ceil_div(g.N, 128) * ceil_div(g.M, 128) * g.shares;
+        if (tiles >= (sizeof(T) == 2 ? 128 : 384)) launch(std::integral_constant<int, 128>{}, std::false_type{});
+        else launch(std::integral_constant<int, 32>{}, std::true_type{});
+    });
+}
+
+static void any_logits(int dtype, const LossArgs& g, int v0, int n, int width, float* logits, hipStream_t st) {
+    const size_t es = dtype_size(dtype);
+    AnyProduct p{};
+    p.a = g.x;
+    p.b = (const char*)g.w + (size_t)v0 * g.D * es;
+    p.bias = g.bias ? (const char*)g.bias + (size_t)v0 * es : nullptr;
+    p.M = g.T, p.N = n, p.K = g.D, p.lda = g.D, p.ldb = g.D;
+    p.c = logits, p.ldc = width;
+    p.shares = 1;
+    launch_any_product<kFormY, false>(dtype, p, st);
+}
+
+// ---- rows of logits ---------------------------------------------------------------
+
+// Adds b's maximum and sum of exponentials about it to a's.
+struct MaxSum {
+    float m, s;
+};
+LS_DEV MaxSum merge(MaxSum a, MaxSum b) {
+    const float m = fmaxf(a.m, b.m);
+    // nothing but -inf so far (or a sum that is NaN: it stays)
+    const float ea = a.m == m ? a.s : a.s * __builtin_amdgcn_exp2f((a.m - m) * kLog2e);
+    const float eb = b.m == m ? b.s : b.s * __builtin_amdgcn_exp2f((b.m - m) * kLog2e);
+    return {m, ea + eb};
+}
+template <int D>
+LS_DEV MaxSum merge_lanes(MaxSum a) {
+    return merge(a, {__uint_as_float(xor_lane<D>(__float_as_uint(a.m))), __uint_as_float(xor_lane<D>(__float_as_uint(a.s)))});
+}
+
+// a row of a piece, one workgroup: its pair, and the target's logit
+__global__ __launch_bounds__(256) void k_loss_part(const float* __restrict__ z, const int64_t* __restrict__ target,
+                                                   int T, int V, int v0, int n, int ld, float2* __restrict__ pairs,
+                                                   float* __restrict__ zt) {
+    __shared__ MaxSum s[4];
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        const float* row = z + (long long)t * ld;
+        MaxSum a{-__builtin_inff(), 0.0f};
+        for (int c = threadIdx.x; c < n; c += 256) a = merge(a, {row[c], row[c] == -__builtin_inff() ? 0.0f : 1.0f});
+        a = merge_lanes<32>(a);
+        a = merge_lanes<16>(a);
+        a = merge_lanes<8>(a);
+        a = merge_lanes<4>(a);
+        a = merge_lanes<2>(a);
+        a = merge_lanes<1>(a);
+        if (lane_id() == 0) s[threadIdx.x >> 6] = a;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            a = merge(merge(s[0], s[1]), merge(s[2], s[3]));
+            pairs[t] = make_float2(a.m, a.s);
+            const int64_t at = target[t] - v0;
+            if (target[t] >= 0 && target[t] < V && at >= 0 && at < n) zt[t] = row[at];
+        }
+        __syncthreads();
+    }
+}
+
+// d of a piece from its logits (in their place, or as 16-bit rows)
+template <class T>
+__global__ __launch_bounds__(256) void k_loss_d(const float* z, const int64_t* __restrict__ target, const float* __restrict__ lse,
+                                                const float* __restrict__ g, int rows, int V, int v0, int n, int ld,
+                                                T* d) {
+    for (long long t = blockIdx.y; t < rows; t += gridDim.y) {
+        const float gt = g[t], l = lse[t];
+        const int64_t at = target[t] - v0;
+        for (int c = blockIdx.x * 256 + threadIdx.x; c < n; c += gridDim.x * 256) {
+            const float p = __builtin_amdgcn_exp2f((z[t * ld + c] - l) * kLog2e);
+            // an ignored row has no gradient, whatever its logits are
+            d[t * ld + c] = from_f<T>(gt == 0.0f ? 0.0f : (p - (at == c ? 1.0f : 0.0f)) * gt);
+        }
+    }
+}
+
+// ---- rows and sums -------------------------------------------------------------------
+
+// A row's pairs merged, 16 rows a workgroup and 16 lanes a row.
+__global__ __launch_bounds__(256) void k_loss_rows(const float2* __restrict__ pairs, int parts,
+                                                   const int64_t* __restrict__ target, const float* __restrict__ zt,
+                                                   int T, int V, float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ MaxSum s[16][17];
+    const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
+    for (long long t0 = (long long)blockIdx.x * 16; t0 < T; t0 += (long long)gridDim.x * 16) {
+        const long long t = t0 + r;
+        MaxSum a{-__builtin_inff(), 0.0f};
+        if (t < T) {
+            int p = q;
+            for (; p + 7 * 16 < parts; p += 8 * 16) {
+                float2 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = pairs[(long long)(p + u * 16) * T + t];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) a = merge(a, {v[u].x, v[u].y});
+            }
+            for (; p < parts; p += 16) {
+                const float2 v = pairs[(long long)p * T + t];
+                a = merge(a, {v.x, v.y});
+            }
+        }
+        s[q][r] = a;
+        __syncthreads();
+        if (q == 0 && t < T) {
+#pragma unroll
+            for (int i = 1; i < 16; ++i) a = merge(a, s[i][r]);
+            const float l = a.m + logf(a.s);
+            if (lse) lse[t] = l;
+            if (loss) loss[t] = target[t] >= 0 && target[t] < V ? l - zt[t] : 0.0f;
+        }
+        __syncthreads();
+    }
+}
+
+void launch_loss_rows(const LossArgs& g, const LossParts& p, char* scratch, float* loss, float* lse, hipStream_t st) {
+    if (g.T < 1) return;
+    hipLaunchKernelGGL(k_loss_rows, dim3(grid_of(ceil_div(g.T, 16))), dim3(256), 0, st,
+                       (const float2*)(scratch + p.pairs), p.parts, g.target, (const float*)(scratch + p.zt), g.T, g.V,
+                       loss, lse);
+}
+
+// Sum or mean of the rows' losses, one workgroup: fp64 lanes' sums, in the
+// order of the lanes.
+__global__ __launch_bounds__(1024) void k_loss_reduce(const float* __restrict__ loss, const int64_t* __restrict__ target,
+                                                      int T, int V, int mean, float* __restrict__ out) {
+    __shared__ double s[16], c[16];
+    double sum = 0.0, count = 0.0;
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        sum += (double)loss[t];
+        count += target[t] >= 0 && target[t] < V ? 1.0 : 0.0;
+    }
+    sum = wave_sum(sum);
+    count = wave_sum(count);
+    if (lane_id() == 0) s[threadIdx.x >> 6] = sum, c[threadIdx.x >> 6] = count;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int i = 1; i < 16; ++i) sum += s[i], count += c[i];
+    *out = (float)(mean ? sum / (count > 0.0 ? count : 1.0) : sum);
+}
+void launch_loss_reduce(const LossArgs& g, const float* loss, int reduction, float* out, hipStream_t st) {
+    hipLaunchKernelGGL(k_loss_reduce, dim3(1), dim3(1024), 0, st, loss, g.target, g.T, g.V, reduction == kReduceMean,
+                       out);
+}
+
+// The gradient of every row's loss, 0 for an ignored row, one workgroup.
+// SCALED (fp16): times the power of two that brings the largest to 2^13 ..
+// 2^14; its inverse stands behind them.
+template <bool SCALED>
+__global__ __launch_bounds__(1024) void k_loss_grad_rows(const float* __restrict__ dloss, const int64_t* __restrict__ target,
+                                                         int T, int V, int reduction, float* __restrict__ g) {
+    __shared__ uint32_t s[16], c[16];
+    uint32_t top = 0, count = 0;
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const bool on = target[t] >= 0 && target[t] < V;
+        count += on;
+        // finite magnitudes, ordered as their bits
+        const uint32_t u = __float_as_uint(dloss[reduction == kReduceNone ? t : 0]) & 0x7FFFFFFFu;
+        if (on && u < 0x7F800000u) top = max(top, u);
+    }
+    count = (uint32_t)wave_sum_u64(count);
+    top = wave_max_u32(top);
+    if (lane_id() == 0) s[threadIdx.x >> 6] = top, c[threadIdx.x >> 6] = count;
+    __syncthreads();
+    for (int i = 0; i < 16; ++i) top = max(top, s[i]);
+    count = 0;
+    for (int i = 0; i < 16; ++i) count += c[i];
+    const float div = reduction == kReduceMean ? (float)max(count, 1u) : 1.0f;
+    int e = 0;
+    if (SCALED && top) {
+        e = 13 - (ilogbf(__uint_as_float(top) / div));
+        e = min(max(e, -100), 100);
+    }
+    const float scale = ldexpf(1.0f, e);
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const bool on = target[t] >= 0 && target[t] < V;
+        g[t] = on ? dloss[reduction == kReduceNone ? t : 0] / div * scale : 0.0f;
+    }
+    if (threadIdx.x == 0) g[T] = ldexpf(1.0f, -e);
+}
+void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int reduction, float* rows,
+                           hipStream_t st) {
+    if (dtype == kF16)
+        hipLaunchKernelGGL(k_loss_grad_rows<true>, dim3(1), dim3(1024), 0, st, dloss, g.target, g.T, g.V, reduction, rows);
+    else
+        hipLaunchKernelGGL(k_loss_grad_rows<false>, dim3(1), dim3(1024), 0, st, dloss, g.target, g.T, g.V, reduction, rows);
+}
+
+// Column sums of a piece's d, 64 columns a workgroup: a wave adds every
+// sixteenth row, and the waves' sums are added in wave order.
+template <class T>
+__global__ __launch_bounds__(1024) void k_loss_db(const T* __restrict__ d, int ld, int rows, int n,
+                                                  const float* __restrict__ unscale, T* __restrict__ db) {
+    __shared__ float s[16][64];
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6), c = blockIdx.x * 64 + l;
+    float sum = 0.0f;
+    if (c < n) {
+#pragma unroll 8
+        for (int t = w; t < rows; t += 16) sum += to_f(d[(long long)t * ld + c]);
+    }
+    s[w][l] = sum;
+    __syncthreads();
+    if (w || c >= n) return;
+    for (int i = 1; i < 16; ++i) sum += s[i][l];
+    db[c] = from_f<T>(sum * *unscale);
+}
+void launch_loss_db(int dtype, const void* d, int ld, int T, int n, const float* unscale, void* db, hipStream_t st) {
+    with_dtype(dtype, [&](auto tv) {
+        using X = decltype(tv);
+        hipLaunchKernelGGL(k_loss_db<X>, dim3((unsigned)ceil_div(n, 64)), dim3(1024), 0, st, (const X*)d, ld, T, n,
+                           unscale, (X*)db);
+    });
+}
+
+// dx from its shares' partial sums, in their order
+template <class T>
+__global__ __launch_bounds__(256) void k_loss_dx(const float* __restrict__ part, int shares, long long n,
+                                                 const float* __restrict__ unscale, T* __restrict__ dx) {
+    const float u = *unscale;
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x); i < n; i += (long long)gridDim.x * 256) {
+        float sum = part[i];
+        for (int s = 1; s < shares; ++s) sum += part[(long long)s * n + i];
+        dx[i] = from_f<T>(sum * u);
+    }
+}
+void launch_loss_dx(int dtype, const float* part, int shares, long long n, const float* unscale, void* dx,
+                    hipStream_t st) {
+    if (n < 1) return;
+    with_dtype(dtype, [&](auto tv) {
+        using X = decltype(tv);
+        hipLaunchKernelGGL(k_loss_dx<X>, dim3((unsigned)std::min(ceil_div(n, 256), 1ll << 16)), dim3(256), 0, st, part,
+                           shares, n, unscale, (X*)dx);
+    });
+}
+
+// ---- the passes --------------------------------------------------------------------
+
+void launch_loss_any(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st) {
+    float* logits = (float*)(scratch + p.logits);
+    for (int i = 0; i < p.parts && g.T > 0; ++i) {
+        const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
+        any_logits(dtype, g, v0, n, p.width, logits, st);
+        hipLaunchKernelGGL(k_loss_part, dim3(grid_of(g.T)), dim3(256), 0, st, logits, g.target, g.T, g.V, v0, n, p.width,
+                           (float2*)(scratch + p.pairs) + (long long)i * g.T, (float*)(scratch + p.zt));
+    }
+}
+
+void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, const float* lse, char* scratch, void* dx,
+                         void* dw, void* db, hipStream_t st) {
+    const size_t es = dtype_size(dtype);
+    float *rows = (float*)(scratch + p.g), *logits = (float*)(scratch + p.logits);
+    const float* unscale = rows + g.T;
+    const bool part = p.pieces * p.shares > 1;
+    for (int i = 0; i < p.pieces; ++i) {
+        const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
+        any_logits(dtype, g, v0, n, p.width, logits, st);
+        const dim3 grid((unsigned)std::min(ceil_div(n, 256), 64ll), (unsigned)std::min(g.T, 65535));
+        with_dtype(dtype, [&](auto tv) {
+            using T = decltype(tv);
+            if (g.T < 1) return;
+            hipLaunchKernelGGL(k_loss_d<T>, grid, dim3(256), 0, st, logits, g.target, lse, rows, g.T, g.V, v0, n, p.width,
+                               (T*)(scratch + p.d));
+        });
+        if (db) launch_loss_db(dtype, scratch + p.d, p.ld, g.T, n, unscale, (char*)db + (size_t)v0 * es, st);
+        AnyProduct q{};
+        q.a = scratch + p.d;
+        q.lda = p.ld;
+        q.unscale = unscale;
+        if (dx) {
+            q.b = (const char*)g.w + (size_t)v0 * g.D * es;
+            q.M = g.T, q.N = g.D, q.K = n, q.ldb = g.D, q.ldc = g.D;
+            q.c = part ? scratch + p.dx : dx;
+            q.shares = p.shares;
+            q.add = i > 0;
+            if (part) launch_any_product<kFormDx, true>(dtype, q, st);
+            else launch_any_product<kFormDx, false>(dtype, q, st);
+        }
+        if (dw) {
+            q.b = g.x;
+            q.M = n, q.N = g.D, q.K = g.T, q.ldb = g.D, q.ldc = g.D;
+            q.c = (char*)dw + (size_t)v0 * g.D * es;
+            q.shares = 1;
+            launch_any_product<kFormDw, false>(dtype, q, st);
+        }
+    }
+    if (dx && part) launch_loss_dx(dtype, (const float*)(scratch + p.dx), p.shares, (long long)g.T * g.D, unscale, dx, st);
+}
+
+}  // namespace lapsum

@@ -1,0 +1,320 @@
+// Softmax cross entropy of 16-bit rows whose width is a multiple of 8: tiles in
+// LDS and 16-bit matrix instructions (lapsum_tile_mfma.h), fp32 sums.
+//
+// Forward, a tile of logits stays in registers: a wave reduces its half of the
+// tile's columns to a row's maximum and sum of exponentials, 8 bytes a row for
+// BN / 2 columns, and the target's logit is written by the lane that holds it.
+// Backward, the same tile becomes d, rounded to 16 bits, in scratch: a piece of
+// the vocabulary at a time, small enough that the products that follow, dx +=
+// d W and dW = d^T x, find it in the memory-side cache.
+#include "lapsum_layer_ops.h"
+#include "lapsum_tile_mfma.h"
+
+namespace lapsum {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr long long kPieceBytes = 256ll << 20;  // of d
+
+static size_t take(size_t& at, size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return here;
+}
+
+bool loss_tile_takes(int dtype, const LossArgs& g) {
+    if (dtype == kF32 || g.D % 8 || g.D < 8 || g.D > (1 << 20) || g.T < 1 || !aligned16(g.x) || !aligned16(g.w))
+        return false;
+    return ceil_div(g.T, 64) * ceil_div(g.V, 64) < 16 * kGridMax;  // one tile a workgroup
+}
+
+// The side of a product's tiles: wide ones where they fill the CUs.
+static int side_of(long long M, long long N) {
+    if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return 256;
+    return ceil_div(M, 128) * ceil_div(N, 128) >= 128 ? 128 : 64;
+}
+template <class F>
+static void with_side(int side, F&& f) {
+    if (side == 256) f(std::integral_constant<int, 256>{});
+    else if (side == 128) f(std::integral_constant<int, 128>{});
+    else f(std::integral_constant<int, 64>{});
+}
+
+// Which tile of `rows` x `cols` a workgroup forms: four row tiles walk the
+// columns together, XCD by XCD (take_turn).
+struct TileAt {
+    int i, j;  // -1: none
+    int quarter;
+};
+LS_DEV TileAt tile_at(int rows, int cols, bool cut) {
+    constexpr int kGroup = 4;
+    const Turn t = take_turn(blockIdx.x, rows * cols, cut);
+    if (t.tile < 0) return {-1, -1, -1};
+    const int first = t.tile / (kGroup * cols) * kGroup, n = min(kGroup, rows - first);
+    const int in = t.tile - first * cols;
+    return {first + in % n, in / n, t.quarter};
+}
+
+// ---- forward ---------------------------------------------------------------------
+
+LossParts loss_tile_parts(const LossArgs& g) {
+    LossParts p{};
+    const int side = side_of(g.T, g.V);
+    p.parts = 2 * (int)ceil_div(g.V, side);
+    size_t at = 0;
+    p.pairs = take(at, (size_t)p.parts * g.T * sizeof(float2));
+    p.zt = take(at, (size_t)g.T * 4);
+    p.loss = take(at, (size_t)g.T * 4);
+    p.bytes = at;
+    return p;
+}
+
+// v += bias, eight columns from j of n
+template <class T>
+LS_DEV void add_bias(float (&v)[8], const T* bias, int j, int n) {
+    if (!bias) return;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] += j + r < n ? to_f(bias[j + r]) : 0.0f;
+}
+LS_DEV float across16(float v, bool max_) {  // over the four lanes that share a row
+    float o = __uint_as_float(xor_lane<16>(__float_as_uint(v)));
+    v = max_ ? fmaxf(v, o) : v + o;
+    o = __uint_as_float(xor_lane<32>(__float_as_uint(v)));
+    return max_ ? fmaxf(v, o) : v + o;
+}
+
+template <class T, int B>
+__global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int rows, int cols, float2* __restrict__ pairs,
+                                                               float* __restrict__ zt) {
+    using Tile = TileSums<T, true, true, B, B>;
+    __shared__ __align__(1024) char lds[Tile::kLds];
+    const TileAt at = tile_at(rows, cols, false);
+    if (at.i < 0) return;
+    const int i0 = at.i * B, j0 = at.j * B, M = g.T - i0, N = g.V - j0;
+    Tile tile;
+    tile.run((const T*)g.x + (long long)i0 * g.D, M, g.D, (const T*)g.w + (long long)j0 * g.D, N, g.D, g.D, lds);
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+    const int r0 = (w >> 1) * (B / 2), c0 = (w & 1) * (B / 2);
+    const T* bias = g.bias ? (const T*)g.bias + j0 : nullptr;
+    // a lane's columns: 8 (l / 16) .. + 7 of each 32
+#pragma unroll
+    for (int j = 0; j < Tile::FN; j += 2) {
+        const int col = c0 + j * 16 + (l >> 4) * 8;
+        float b[8] = {};
+        add_bias(b, bias, col, N);
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float v = tile.acc[i][j + (r >> 2)][r & 3];
+                tile.acc[i][j + (r >> 2)][r & 3] = col + r < N ? v + b[r] : -__builtin_inff();
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i) {
+        const int row = r0 + i * 16 + (l & 15);
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m = fmaxf(m, tile.acc[i][j][r]);
+        m = across16(m, true);
+        const float from = m == -__builtin_inff() ? 0.0f : m;
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f((tile.acc[i][j][r] - from) * kLog2e);
+        s = across16(s, false);
+        if (row >= M) continue;
+        const int part = at.j * 2 + (w & 1);
+        if (l < 16) pairs[(long long)part * g.T + i0 + row] = make_float2(m, s);
+        // the target, if this lane holds it
+        const int64_t target = g.target[i0 + row];
+        const int64_t c = target - j0 - c0;
+        if (target < 0 || target >= g.V || c < 0 || c >= B / 2 || (c & 31) >> 3 != l >> 4) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (c == (j >> 1) * 32 + (l >> 4) * 8 + (j & 1) * 4 + r) v = tile.acc[i][j][r];
+        zt[i0 + row] = v;
+    }
+}
+
+void launch_loss_tile(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st) {
+    with_side(side_of(g.T, g.V), [&](auto bv) {
+        constexpr int B = bv.value;
+        const long long rows = ceil_div(g.T, B), cols = ceil_div(g.V, B);
+        with_dtype(dtype, [&](auto tv) {
+            using T = decltype(tv);
+            if constexpr (sizeof(T) == 2)
+                hipLaunchKernelGGL((k_loss_tile<T, B>), dim3((unsigned)turns(rows * cols, false)), dim3(kProductThreads), 0,
+                                   st, g, (int)rows, (int)cols, (float2*)(scratch + p.pairs), (float*)(scratch + p.zt));
+        });
+    });
+}
+
+// ---- backward --------------------------------------------------------------------
+
+LossVjpPlan loss_tile_plan(const LossArgs& g) {
+    LossVjpPlan p{};
+    const long long most = std::max(kPieceBytes / 2 / std::max(g.T, 1) / 256 * 256, 256ll);
+    p.width = (int)std::min<long long>(std::min(most, 1ll << 18), g.V);
+    p.ld = (p.width + 7) & ~7;
+    p.pieces = (int)ceil_div(g.V, p.width);
+    // dx's sum over a piece is shared out where its tiles are few
+    const long long tiles = ceil_div(g.T, 64) * ceil_div(g.D, 64);
+    p.shares = (int)std::max(1ll, std::min<long long>(512 / tiles, p.width / 512));
+    size_t at = 0;
+    p.g = take(at, ((size_t)g.T + 1) * 4);
+    p.d = take(at, (size_t)g.T * p.ld * 2);
+    if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
+    p.bytes = at;
+    return p;
+}
+
+// d of the columns v0 .. v0 + n - 1, zeros up to a multiple of 8
+template <class T, int B>
+__global__ __launch_bounds__(kProductThreads) void k_loss_dtile(LossArgs g, int v0, int n, int ld, int rows, int cols,
+                                                                const float* __restrict__ lse,
+                                                                const float* __restrict__ grad, T* __restrict__ d) {
+    using Tile = TileSums<T, true, true, B, B>;
+    __shared__ __align__(1024) char lds[Tile::kLds];
+    const TileAt at = tile_at(rows, cols, false);
+    if (at.i < 0) return;
+    const int i0 = at.i * B, j0 = at.j * B, M = g.T - i0, N = n - j0;
+    Tile tile;
+    tile.run((const T*)g.x + (long long)i0 * g.D, M, g.D, (const T*)g.w + (long long)(v0 + j0) * g.D, N, g.D, g.D, lds);
+    const T* bias = g.bias ? (const T*)g.bias + v0 + j0 : nullptr;
+    struct __attribute__((aligned(16))) T8 { T v[8]; };
+    tile.each8([&](int row, int col, float (&v)[8]) {
+        if (row >= M || col >= ((N + 7) & ~7)) return;
+        add_bias(v, bias, col, N);
+        const float gt = grad[i0 + row], l = lse[i0 + row];
+        const int64_t hit = g.target[i0 + row] - v0 - j0 - col;
+        T8 o;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float p = __builtin_amdgcn_exp2f((v[r] - l) * kLog2e);
+            // an ignored row has no gradient, whatever its logits are
+            o.v[r] = from_f<T>(gt == 0.0f || col + r >= N ? 0.0f : (p - (hit == r ? 1.0f : 0.0f)) * gt);
+        }
+        *(T8*)(d + (long long)(i0 + row) * ld + j0 + col) = o;
+    });
+}
+
+struct LossProduct {
+    const void *a, *b;
+    int M, N, K, lda, ldb;
+    int own_a;            // a's rows that can be read
+    void* c;
+    const float* unscale;
+    int shares;           // of K: partial sums, M * N elements apart
+    int share;            // k of a share, a multiple of 64
+    bool add;
+};
+template <class T, bool kA, bool PART, int BM, int BN>
+LS_DEV void product_tile(const LossProduct& g, int i0, int j0, int z, char* lds) {
+    const int k0 = z * g.share, K = min(g.share, g.K - k0);
+    const T* a = (const T*)g.a + (kA ? (long long)i0 * g.lda + k0 : (long long)k0 * g.lda + i0);
+    const T* b = (const T*)g.b + (long long)k0 * g.ldb + j0;
+    const int M = g.M - i0, N = g.N - j0;
+    TileSums<T, kA, false, BM, BN> tile;
+    tile.run(a, g.own_a - i0, g.lda, b, N, g.ldb, K, lds);
+    struct __attribute__((aligned(16))) T8 { T v[8]; };
+    const float unscale = PART ? 1.0f : *g.unscale;
+    tile.each8([&](int row, int col, float (&v)[8]) {
+        if (row >= M || col >= N) return;
+        const long long to = (long long)(i0 + row) * g.N + j0 + col;
+        if constexpr (PART) {
+            f32x4* p = (f32x4*)((float*)g.c + (long long)z * g.M * g.N + to);
+            f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+            if (g.add) lo += p[0], hi += p[1];
+            p[0] = lo;
+            p[1] = hi;
+        } else {
+            T8 o;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) o.v[r] = from_f<T>(v[r] * unscale);
+            *(T8*)((T*)g.c + to) = o;
+        }
+    });
+}
+template <class T, bool kA, bool PART, int B>
+__global__ __launch_bounds__(kProductThreads) void k_loss_product(LossProduct g, int rows, int cols) {
+    __shared__ __align__(1024) char lds[TileSums<T, kA, false, B, B>::kLds];
+    const TileAt at = tile_at(rows, cols, B == 256);
+    if (at.i < 0) return;
+    int i0 = at.i * B, j0 = at.j * B;
+    if constexpr (B == 256) {
+        if (at.quarter >= 0) {
+            i0 += (at.quarter >> 1) * (B / 2);
+            j0 += (at.quarter & 1) * (B / 2);
+            if (i0 < g.M && j0 < g.N) product_tile<T, kA, PART, B / 2, B / 2>(g, i0, j0, blockIdx.y, lds);
+            return;
+        }
+    }
+    product_tile<T, kA, PART, B, B>(g, i0, j0, blockIdx.y, lds);
+}
+
+template <bool kA, bool PART>
+static void launch_product(int dtype, LossProduct& g, hipStream_t st) {
+    g.share = (int)(ceil_div(ceil_div(g.K, g.shares), 64) * 64);
+    with_side(side_of(g.M, g.N), [&](auto bv) {
+        constexpr int B = bv.value;
+        const long long rows = ceil_div(g.M, B), cols = ceil_div(g.N, B);
+        with_dtype(dtype, [&](auto tv) {
+            using T = decltype(tv);
+            if constexpr (sizeof(T) == 2)
+                hipLaunchKernelGGL((k_loss_product<T, kA, PART, B>),
+                                   dim3((unsigned)turns(rows * cols, B == 256), (unsigned)g.shares), dim3(kProductThreads),
+                                   0, st, g, (int)rows, (int)cols);
+        });
+    });
+}
+
+void launch_loss_tile_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, const float* lse, char* scratch,
+                          void* dx, void* dw, void* db, hipStream_t st) {
+    float* rows = (float*)(scratch + p.g);
+    const float* unscale = rows + g.T;
+    const bool part = p.pieces * p.shares > 1;
+    for (int i = 0; i < p.pieces; ++i) {
+        const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
+        with_side(side_of(g.T, n), [&](auto bv) {
+            constexpr int B = bv.value;
+            const long long r = ceil_div(g.T, B), c = ceil_div(n, B);
+            with_dtype(dtype, [&](auto tv) {
+                using T = decltype(tv);
+                if constexpr (sizeof(T) == 2)
+                    hipLaunchKernelGGL((k_loss_dtile<T, B>), dim3((unsigned)turns(r * c, false)), dim3(kProductThreads),
+                                       0, st, g, v0, n, p.ld, (int)r, (int)c, lse, rows, (T*)(scratch + p.d));
+            });
+        });
+        if (db) launch_loss_db(dtype, scratch + p.d, p.ld, g.T, n, unscale, (char*)db + (size_t)v0 * 2, st);
+        LossProduct q{};
+        q.a = scratch + p.d;
+        q.lda = p.ld;
+        q.unscale = unscale;
+        if (dx) {
+            q.b = (const char*)g.w + (size_t)v0 * g.D * 2;
+            q.M = q.own_a = g.T, q.N = g.D, q.K = n, q.ldb = g.D;
+            q.c = part ? scratch + p.dx : dx;
+            q.shares = p.shares;
+            q.add = i > 0;
+            if (part) launch_product<true, true>(dtype, q, st);
+            else launch_product<true, false>(dtype, q, st);
+        }
+        if (dw) {
+            q.b = g.x;
+            q.M = n, q.own_a = (n + 7) & ~7, q.N = g.D, q.K = g.T, q.ldb = g.D;
+            q.c = (char*)dw + (size_t)v0 * g.D * 2;
+            q.shares = 1;
+            q.add = false;
+            launch_product<false, false>(dtype, q, st);
+        }
+    }
+    if (dx && part) launch_loss_dx(dtype, (const float*)(scratch + p.dx), p.shares, (long long)g.T * g.D, unscale, dx, st);
+}
+
+}  // namespace lapsum

@@ -1,0 +1,372 @@
+// The experts' products on rows and weights in 8 bits: e4m3 values in blocks of
+// 128 along the sum, each under a power of two.
+//
+// Mathematics: y(i, j) = act(sum over blocks b of 2^(ea(i, b) + eb(j, b)) times
+// the sum over k of b of qa(i, k) qb(j, k), + bias(j)), i over one expert's
+// rows.  The matrix instruction v_mfma_scale_f32_32x32x64_f8f6f4 takes the two
+// powers of two of each row from registers and multiplies them in, so the
+// blocks' sums run on in one fp32 accumulator.
+//
+// The tiles are those of the 16-bit products (lapsum_tile_mfma.h): four waves,
+// a quarter of a B x B tile each, operands straight from memory to a ring of
+// five LDS buffers of 64 bytes of k.  A step is one matrix instruction deep (64
+// k), two steps are a block, and a row is whole blocks, so no load is masked
+// along the sum.
+//  - Scales stay in registers, 16 blocks' of each row that a lane multiplies,
+//    shifted on by a byte a block; the next 16 are fetched after 2048 k.
+//  - A weight fragment's rows are dealt out so that a lane's 16 sums of one
+//    row are 16 consecutive columns.
+//
+// Accuracy.  Of eight neighbouring products that instruction drops what is 2^14
+// and more below the largest (measured: a product of 2^-13 of the largest is
+// kept, one of 2^-14 is not; between groups of eight, and into the accumulator,
+// fp32), which leaves sums of random rows 1.5e-5 off in the 2-norm, whatever
+// their length: a thirtieth of fp16's rounding.  Results in fp32 take the bf16
+// instruction instead, on values expanded in registers, scales and all: e4m3
+// fits bf16, so the products are exact and the sums fp32's own.
+#include "lapsum_layer_ops.h"
+#include "lapsum_tile_mfma.h"
+
+namespace lapsum {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
+
+constexpr int kStep8 = 64;  // k of one LDS buffer
+
+// One operand of a tile: R rows by kStep8 of k.  COLS: its rows are the
+// product's columns, dealt out to a fragment as above.
+template <int R, bool COLS>
+struct Operand8 {
+    static constexpr int kBytes = R * 64;
+    static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads per step
+
+    const char* base;  // the tile's first row
+    uint32_t bytes;    // of the rows that exist
+    uint32_t voff[kLoads];
+
+    // A row has 4 chunks of 16 bytes, two rows lie in a line of 128; a row's
+    // chunk c lies at c ^ fold(line).  Eight lanes that read one chunk of
+    // neighbouring fragment rows then meet no bank twice.
+    static LS_DEV int fold(int line) { return COLS ? (line & 1) | (line >> 2 & 2) : line & 3; }
+
+    LS_DEV void init(const uint8_t* x, int own, uint32_t ld) {
+        base = reinterpret_cast<const char*>(x);
+        bytes = (uint32_t)min(R, own) * ld;
+        const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int line = (w * kLoads + i) * 8 + (l >> 3), u = (l & 7) ^ fold(line);
+            voff[i] = (uint32_t)(line * 2 + (u >> 2)) * ld + (u & 3) * 16;
+        }
+    }
+    // the buffer of k0 .. (empty past K: its loads write zeros)
+    LS_DEV u32x4 window(int k0, int K) const {
+        const char* p = base + k0;
+        return u32x4{(uint32_t)(uintptr_t)p, (uint32_t)((uintptr_t)p >> 32), k0 < K ? bytes - (uint32_t)k0 : 0u,
+                     0x00020000u};
+    }
+    LS_DEV void load(const u32x4& win, uint32_t lds, int i) const {
+        load_to_lds(win, voff[i], lds + (uniform(threadIdx.x >> 6) * kLoads + i) * 1024);
+    }
+    // the row of the operand that lane l has of fragment f of the rows from r0
+    static LS_DEV int row(int r0, int f) {
+        const int s = lane_id() & 31;
+        return r0 + f * 32 + (COLS ? (s >> 2 & 1) * 16 + (s >> 3) * 4 + (s & 3) : s);
+    }
+    // half h of it: chunk 2 (l / 32) + h of its row
+    static LS_DEV u32x4 half(const char* lds, int r0, int f, int h) {
+        const int r = row(r0, f), c = (lane_id() >> 5) * 2 + h;
+        return *(const u32x4*)(lds + (r >> 1) * 128 + (((r & 1) * 4 + c) ^ fold(r >> 1)) * 16);
+    }
+};
+
+// 16 blocks' scales of a row from block b, of an array with `left` bytes from
+// the row's first; bytes past the row are never used
+LS_DEV u32x4 scales16(const uint8_t* row, int b, long long left) {
+    if (b + 16 <= left) return *reinterpret_cast<const u32x4u*>(row + b);
+    uint32_t v[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (b + i < left) v[i >> 2] |= (uint32_t)row[b + i] << (i & 3) * 8;
+    return u32x4{v[0], v[1], v[2], v[3]};
+}
+
+// 16 values (a half of a fragment) under the power of two of scale byte 0, in bf16
+LS_DEV void expand(bf16x8 (&o)[2], u32x4 v, uint32_t scale) {
+    const float by = __uint_as_float((scale & 255u) << 23);  // the exponent is all that counts
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[w], by, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[w], by, true);
+        const int at = (w & 1) * 4;
+        o[w >> 1][at] = lo[0], o[w >> 1][at + 1] = lo[1], o[w >> 1][at + 2] = hi[0], o[w >> 1][at + 3] = hi[1];
+    }
+}
+
+// EXACT: by the bf16 instruction
+template <int BM, int BN, bool EXACT>
+struct TileSums8 {
+    using OpA = Operand8<BM, false>;
+    using OpB = Operand8<BN, true>;
+    static constexpr int FM = BM / 64, FN = BN / 64;  // fragments of a wave
+    static constexpr int kBuffer = OpA::kBytes + OpB::kBytes;
+    static constexpr int kLds = kRing * kBuffer;
+
+    f32x16 acc[FM][FN] = {};
+
+    // a, as: the tile's first row and its scales, M rows from there; b, bs, N
+    // the same of its columns; left_a, left_b: scales from there to the array's end
+    LS_DEV void run(const uint8_t* a, const uint8_t* as, int M, long long left_a, const uint8_t* b, const uint8_t* bs,
+                    int N, long long left_b, int blocks, char* lds) {
+        const int K = blocks * kBlock8, w = uniform(threadIdx.x >> 6);
+        const int r0 = (w >> 1) * (BM / 2), c0 = (w & 1) * (BN / 2);
+        OpA oa;
+        OpB ob;
+        oa.init(a, M, (uint32_t)K);
+        ob.init(b, N, (uint32_t)K);
+        u32x4 sa[FM], sb[FN];
+        auto scales = [&](int blk) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const long long at = (long long)min(OpA::row(r0, i), M - 1) * blocks;
+                sa[i] = scales16(as + at, blk, left_a - at);
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const long long at = (long long)min(OpB::row(c0, j), N - 1) * blocks;
+                sb[j] = scales16(bs + at, blk, left_b - at);
+            }
+        };
+        scales(0);
+        const uint32_t at = (uint32_t)(uintptr_t)(LS_LDS(char)*)lds;
+        // steps s and s + 1 of one operand, interleaved, loads [from, to)
+        auto fetch = [&](const auto& op, const u32x4 (&win)[2], uint32_t to0, uint32_t to1, int from, int to) {
+#pragma unroll
+            for (int r = from; r < to; ++r) {
+                if (r & 1) op.load(win[1], to1, r >> 1);
+                else op.load(win[0], to0, r >> 1);
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+            const int k0 = q * kStep8;
+            const u32x4 wa[2] = {oa.window(k0, K), oa.window(k0 + kStep8, K)};
+            const u32x4 wb[2] = {ob.window(k0, K), ob.window(k0 + kStep8, K)};
+            const uint32_t to = at + q * kBuffer;
+            fetch(oa, wa, to, to + kBuffer, 0, 2 * OpA::kLoads);
+            fetch(ob, wb, to + OpA::kBytes, to + OpA::kBytes + kBuffer, 0, 2 * OpB::kLoads);
+        }
+        u32x4 fa[2][FM][2], fb[2][FN][2];
+        step_barrier<2 * (OpA::kLoads + OpB::kLoads)>();
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) fb[0][j][h] = OpB::half(lds + OpA::kBytes, c0, j, h);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) fa[0][i][h] = OpA::half(lds, r0, i, h);
+        auto whole = [](const u32x4 (&f)[2]) {
+            return __builtin_bit_cast(i32x8, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        // as in the 16-bit tiles: step s multiplies the fragments of set s % 2
+        // and reads step s + 1 into the other; an even step fetches A for s + 4
+        // and s + 5, an odd one B for s + 3 and s + 4
+        int prev2 = 0, prev = 4 * kBuffer, cur = 0, next = kBuffer;
+        auto step = [&](auto qv, int k0) {
+            constexpr int q = decltype(qv)::value;
+            step_barrier<q == 0 ? 63 : 2 * OpA::kLoads>();
+            const char *pa = lds + next, *pb = pa + OpA::kBytes;
+            constexpr int kReads = 2 * (FM + FN), kReadIn = FM > 1 ? FM / 2 : 1;
+            const int kf = k0 + (q == 0 ? 4 : 3) * kStep8;
+            u32x4 win[2];
+            if (q == 0) win[0] = oa.window(kf, K), win[1] = oa.window(kf + kStep8, K);
+            else win[0] = ob.window(kf, K), win[1] = ob.window(kf + kStep8, K);
+            const uint32_t to0 = at + (q == 0 ? prev : prev2 + OpA::kBytes);
+            const uint32_t to1 = at + (q == 0 ? cur : prev + OpA::kBytes);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                if (i < kReadIn) {
+#pragma unroll
+                    for (int r = i * kReads / kReadIn; r < (i + 1) * kReads / kReadIn; ++r) {
+                        const int f = r >> 1;
+                        if (f < FN) fb[q ^ 1][f][r & 1] = OpB::half(pb, c0, f, r & 1);
+                        else fa[q ^ 1][f - FN][r & 1] = OpA::half(pa, r0, f - FN, r & 1);
+                    }
+                }
+                if (q == 0) fetch(oa, win, to0, to1, i * 2 * OpA::kLoads / FM, (i + 1) * 2 * OpA::kLoads / FM);
+                else fetch(ob, win, to0, to1, i * 2 * OpB::kLoads / FM, (i + 1) * 2 * OpB::kLoads / FM);
+                if constexpr (EXACT) {
+                    bf16x8 a[2][2];
+                    expand(a[0], fa[q][i][0], sa[i][0]);
+                    expand(a[1], fa[q][i][1], sa[i][0]);
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        bf16x8 b[2][2];
+                        expand(b[0], fb[q][j][0], sb[j][0]);
+                        expand(b[1], fb[q][j][1], sb[j][0]);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[h >> 1][h & 1], a[h >> 1][h & 1],
+                                                                                acc[i][j], 0, 0, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            whole(fb[q][j]), whole(fa[q][i]), acc[i][j], 0, 0, 0, (int)sb[j][0], 0, (int)sa[i][0]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            prev2 = prev;
+            prev = cur;
+            cur = next;
+            next = next == (kRing - 1) * kBuffer ? 0 : next + kBuffer;
+        };
+        auto on = [](u32x4& s) {  // to the next block's scale
+            s[0] = __builtin_amdgcn_alignbyte(s[1], s[0], 1);
+            s[1] = __builtin_amdgcn_alignbyte(s[2], s[1], 1);
+            s[2] = __builtin_amdgcn_alignbyte(s[3], s[2], 1);
+            s[3] >>= 8;
+        };
+        for (int blk = 0; blk < blocks; ++blk) {
+            step(std::integral_constant<int, 0>{}, blk * kBlock8);
+            step(std::integral_constant<int, 1>{}, blk * kBlock8 + kStep8);
+            if ((blk & 15) == 15) {
+                if (blk + 1 < blocks) scales(blk + 1);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) on(sa[i]);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) on(sb[j]);
+        }
+        // the last steps' loads, past K, still write zeros to LDS
+        step_barrier<0>();
+    }
+};
+
+// V consecutive results of a row from their sums, with V such that they are 16
+// bytes: bias, activation, and stores of 16 bytes where `wide`
+template <class T, int ACT, int V>
+LS_DEV void put8(const float* v, const T* bias, T* c, int col, int N, bool wide) {
+    struct __attribute__((aligned(16))) TV { T v[V]; } o;
+    if (wide) {  // N is a multiple of 16 bytes: all or nothing
+        if (col >= N) return;
+        TV b = {};
+        if (bias) b = *(const TV*)(bias + col);
+#pragma unroll
+        for (int r = 0; r < V; ++r) o.v[r] = from_f<T>(act_of<ACT, T>(v[r] + (bias ? to_f(b.v[r]) : 0.0f)));
+        *(TV*)(c + col) = o;
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < V; ++r)
+        if (col + r < N) c[col + r] = from_f<T>(act_of<ACT, T>(v[r] + (bias ? to_f(bias[col + r]) : 0.0f)));
+}
+
+struct Piece8 {
+    const uint8_t *a, *as, *b, *bs;
+    long long left_a, left_b;
+    const void* bias;
+    void* c;
+    int M, N, blocks;  // blocks: 0 for unused rows
+    bool wide;
+};
+template <class T, int ACT, int BM, int BN>
+LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
+    using Tile = TileSums8<BM, BN, sizeof(T) == 4>;
+    Tile tile;
+    const int M = p.M - i0, N = p.N - j0;
+    if (p.blocks > 0) {
+        const long long a = (long long)i0 * p.blocks, b = (long long)j0 * p.blocks;
+        tile.run(p.a + a * kBlock8, p.as + a, M, p.left_a - a, p.b + b * kBlock8, p.bs + b, N, p.left_b - b, p.blocks,
+                 lds);
+    }
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+    const int r0 = (w >> 1) * (BM / 2), c0 = (w & 1) * (BN / 2);
+    constexpr int V = 16 / (int)sizeof(T);
+    const T* bias = p.bias ? (const T*)p.bias + j0 : nullptr;
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i) {
+        const int row = r0 + i * 32 + (l & 31);
+        if (row >= M) continue;
+        T* c = (T*)p.c + (long long)(i0 + row) * p.N + j0;
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j) {
+            float v[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[r] = tile.acc[i][j][r];
+#pragma unroll
+            for (int q = 0; q < 16; q += V) put8<T, ACT, V>(v + q, bias, c, c0 + j * 32 + (l >> 5) * 16 + q, N, p.wide);
+        }
+    }
+}
+
+template <class T, int ACT, int B>
+__global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g, bool wide) {
+    constexpr int kGroup = 4;  // row tiles that walk the columns together
+    constexpr bool kCut = B == 256;
+    __shared__ __align__(1024) char lds[TileSums8<B, B, false>::kLds];
+    const int cols = (g.out + B - 1) / B;
+    RowTiles<B> rows(g.off, g.E, g.P);
+    const Turn t = take_turn(blockIdx.x, rows.count() * cols, kCut);
+    if (t.tile < 0) return;
+    const RowTile at = rows.find(t.tile / cols);
+    const bool used = at.e < g.E;
+    const long long e = used ? at.e : 0, row = (long long)g.blocks, mat = (long long)g.out * g.blocks;
+    Piece8 p;
+    p.M = at.ehi - at.elo;
+    p.N = g.out;
+    p.blocks = used ? g.blocks : 0;  // unused rows: zeros
+    p.a = g.a + at.elo * row * kBlock8;
+    p.as = g.as + at.elo * row;
+    p.left_a = (g.P - at.elo) * row;
+    p.b = g.b + e * mat * kBlock8;
+    p.bs = g.bs + e * mat;
+    p.left_b = (g.E - e) * mat;
+    p.bias = g.bias && used ? (const T*)g.bias + e * g.out : nullptr;
+    p.c = (T*)g.c + (long long)at.elo * g.out;
+    p.wide = wide;
+    const int q = t.tile - at.first * cols, tiles = (p.M + B - 1) / B;
+    const int first = q / (kGroup * cols) * kGroup, n = min(kGroup, tiles - first), in = q - first * cols;
+    int i0 = (first + in % n) * B, j0 = in / n * B;
+    if constexpr (kCut) {
+        if (t.quarter >= 0) {
+            i0 += (t.quarter >> 1) * (B / 2);
+            j0 += (t.quarter & 1) * (B / 2);
+            if (i0 < p.M && j0 < p.N) tile8<T, ACT, B / 2, B / 2>(p, i0, j0, lds);
+            return;
+        }
+    }
+    tile8<T, ACT, B, B>(p, i0, j0, lds);
+}
+
+void launch_expert_linear8(int dtype, const Linear8Args& g, hipStream_t st) {
+    if (g.P < 1 || g.out < 1) return;
+    const bool wide = (long long)g.out * (long long)dtype_size(dtype) % 16 == 0 && aligned16(g.c) && aligned16(g.bias);
+    with_dtype(dtype, [&](auto tv) {
+        using T = decltype(tv);
+        with_act(g.act, [&](auto av) {
+            auto launch = [&](auto bv) {
+                constexpr int B = bv.value;
+                const long long tiles = max_row_tiles<B>(g.P, g.E) * ceil_div(g.out, B);
+                hipLaunchKernelGGL((k_linear8<T, decltype(av)::value, B>), dim3((unsigned)turns(tiles, B == 256)),
+                                   dim3(kProductThreads), 0, st, g, wide);
+            };
+            const long long per = g.P / g.E;
+            // one tile a workgroup, whose threads a launch counts in 32 bits
+            const bool many = max_row_tiles<64>(g.P, g.E) * ceil_div(g.out, 64) >= kGridMax;
+            // (fp32's expanded fragments leave no registers for the widest)
+            const bool widest = sizeof(T) == 2 && per >= 96 && (g.P / 256 + g.E / 2) * ceil_div(g.out, 256) >= 256;
+            if (many || widest) launch(std::integral_constant<int, 256>{});
+            else if (per > 32 && (g.P / 128 + g.E / 2) * ceil_div(g.out, 128) >= 128)
+                launch(std::integral_constant<int, 128>{});
+            else launch(std::integral_constant<int, 64>{});
+        });
+    });
+}
+
+}  // namespace lapsum
