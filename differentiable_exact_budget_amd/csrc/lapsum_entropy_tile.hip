@@ -95,50 +95,59 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int r
     const int l = lane_id(), w = uniform(threadIdx.x >> 6);
     const int r0 = (w >> 1) * (B / 2), c0 = (w & 1) * (B / 2);
     const T* bias = g.bias ? (const T*)g.bias + j0 : nullptr;
-    // a lane's columns: 8 (l / 16) .. + 7 of each 32
+    int64_t target[Tile::FM];
 #pragma unroll
-    for (int j = 0; j < Tile::FN; j += 2) {
-        const int col = c0 + j * 16 + (l >> 4) * 8;
-        float b[8] = {};
-        add_bias(b, bias, col, N);
+    for (int i = 0; i < Tile::FM; ++i) target[i] = g.target[i0 + min(r0 + i * 16 + (l & 15), M - 1)];
+    // a lane's columns: 8 (l / 16) .. + 7 of each 32; what is added to their
+    // logits, -inf past the vocabulary's end
+    const bool edge = bias || N < B;
+    float add[Tile::FN][4] = {};
+    if (edge) {
 #pragma unroll
-        for (int i = 0; i < Tile::FM; ++i)
+        for (int j = 0; j < Tile::FN; ++j)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float v = tile.acc[i][j + (r >> 2)][r & 3];
-                tile.acc[i][j + (r >> 2)][r & 3] = col + r < N ? v + b[r] : -__builtin_inff();
+            for (int r = 0; r < 4; ++r) {
+                const int col = c0 + (j >> 1) * 32 + (l >> 4) * 8 + (j & 1) * 4 + r;
+                add[j][r] = col >= N ? -__builtin_inff() : bias ? to_f(bias[col]) : 0.0f;
             }
     }
 #pragma unroll
     for (int i = 0; i < Tile::FM; ++i) {
         const int row = r0 + i * 16 + (l & 15);
+        f32x4 v[Tile::FN];
         float m = -__builtin_inff();
 #pragma unroll
-        for (int j = 0; j < Tile::FN; ++j)
+        for (int j = 0; j < Tile::FN; ++j) {
+            v[j] = tile.acc[i][j];
+            if (edge) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) m = fmaxf(m, tile.acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) v[j][r] += add[j][r];
+            }
+            m = fmaxf(m, fmaxf(fmaxf(v[j][0], v[j][1]), fmaxf(v[j][2], v[j][3])));
+        }
         m = across16(m, true);
-        const float from = m == -__builtin_inff() ? 0.0f : m;
+        // m log2 e as it is rounded here cancels in the row's logarithm to within
+        // its own rounding
+        const float from = m == -__builtin_inff() ? 0.0f : m * -kLog2e;
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < Tile::FN; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f((tile.acc[i][j][r] - from) * kLog2e);
+            for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(fmaf(v[j][r], kLog2e, from));
         s = across16(s, false);
         if (row >= M) continue;
         const int part = at.j * 2 + (w & 1);
         if (l < 16) pairs[(long long)part * g.T + i0 + row] = make_float2(m, s);
         // the target, if this lane holds it
-        const int64_t target = g.target[i0 + row];
-        const int64_t c = target - j0 - c0;
-        if (target < 0 || target >= g.V || c < 0 || c >= B / 2 || (c & 31) >> 3 != l >> 4) continue;
-        float v = 0.0f;
+        const int64_t c = target[i] - j0 - c0;
+        if (target[i] < 0 || target[i] >= g.V || c < 0 || c >= B / 2 || (c & 31) >> 3 != l >> 4) continue;
+        float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < Tile::FN; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (c == (j >> 1) * 32 + (l >> 4) * 8 + (j & 1) * 4 + r) v = tile.acc[i][j][r];
-        zt[i0 + row] = v;
+                if (c == (j >> 1) * 32 + (l >> 4) * 8 + (j & 1) * 4 + r) z = v[j][r];
+        zt[i0 + row] = z;
     }
 }
 
@@ -188,20 +197,44 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_dtile(LossArgs g, int 
     tile.run((const T*)g.x + (long long)i0 * g.D, M, g.D, (const T*)g.w + (long long)(v0 + j0) * g.D, N, g.D, g.D, lds);
     const T* bias = g.bias ? (const T*)g.bias + v0 + j0 : nullptr;
     struct __attribute__((aligned(16))) T8 { T v[8]; };
-    tile.each8([&](int row, int col, float (&v)[8]) {
-        if (row >= M || col >= ((N + 7) & ~7)) return;
-        add_bias(v, bias, col, N);
-        const float gt = grad[i0 + row], l = lse[i0 + row];
-        const int64_t hit = g.target[i0 + row] - v0 - j0 - col;
-        T8 o;
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6);
+    const int r0 = (w >> 1) * (B / 2), c0 = (w & 1) * (B / 2);
+    // this lane's rows, all asked for at once
+    float gt[Tile::FM], lo[Tile::FM];
+    int hit[Tile::FM];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const float p = __builtin_amdgcn_exp2f((v[r] - l) * kLog2e);
-            // an ignored row has no gradient, whatever its logits are
-            o.v[r] = from_f<T>(gt == 0.0f || col + r >= N ? 0.0f : (p - (hit == r ? 1.0f : 0.0f)) * gt);
+    for (int i = 0; i < Tile::FM; ++i) {
+        const int t = i0 + min(r0 + i * 16 + (l & 15), M - 1);
+        gt[i] = grad[t];
+        lo[i] = lse[t] * -kLog2e;
+        const int64_t at = g.target[t] - v0 - j0 - c0;
+        hit[i] = at >= 0 && at < B / 2 ? (int)at : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < Tile::FN; j += 2) {
+        const int in = j * 16 + (l >> 4) * 8, col = c0 + in;
+        if (col >= ((N + 7) & ~7)) continue;
+        float b[8] = {};
+        add_bias(b, bias, col, N);
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = r0 + i * 16 + (l & 15);
+            T8 o;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float v = tile.acc[i][j + (r >> 2)][r & 3] + b[r];
+                const float p = __builtin_amdgcn_exp2f(fmaf(v, kLog2e, lo[i])) - (hit[i] == in + r ? 1.0f : 0.0f);
+                // an ignored row has no gradient, whatever its logits are
+                o.v[r] = from_f<T>(gt[i] == 0.0f ? 0.0f : p * gt[i]);
+            }
+            if (col + 8 > N) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (col + r >= N) o.v[r] = from_f<T>(0.0f);
+            }
+            if (row < M) *(T8*)(d + (long long)(i0 + row) * ld + j0 + col) = o;
         }
-        *(T8*)(d + (long long)(i0 + row) * ld + j0 + col) = o;
-    });
+    }
 }
 
 struct LossProduct {

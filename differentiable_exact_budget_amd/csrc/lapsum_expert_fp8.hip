@@ -85,11 +85,14 @@ struct Operand8 {
 // the row's first; bytes past the row are never used
 LS_DEV u32x4 scales16(const uint8_t* row, int b, long long left) {
     if (b + 16 <= left) return *reinterpret_cast<const u32x4u*>(row + b);
-    uint32_t v[4] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (b + i < left) v[i >> 2] |= (uint32_t)row[b + i] << (i & 3) * 8;
-    return u32x4{v[0], v[1], v[2], v[3]};
+    uint64_t v[2] = {};
+#pragma unroll 1
+    for (int i = 0; b + i < left; ++i) {
+        const uint64_t x = (uint64_t)row[b + i] << (i & 7) * 8;
+        if (i < 8) v[0] |= x;
+        else v[1] |= x;
+    }
+    return u32x4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)};
 }
 
 // 16 values (a half of a fragment) under the power of two of scale byte 0, in bf16
@@ -139,7 +142,6 @@ struct TileSums8 {
                 sb[j] = scales16(bs + at, blk, left_b - at);
             }
         };
-        scales(0);
         const uint32_t at = (uint32_t)(uintptr_t)(LS_LDS(char)*)lds;
         // steps s and s + 1 of one operand, interleaved, loads [from, to)
         auto fetch = [&](const auto& op, const u32x4 (&win)[2], uint32_t to0, uint32_t to1, int from, int to) {
@@ -231,40 +233,62 @@ struct TileSums8 {
             s[2] = __builtin_amdgcn_alignbyte(s[3], s[2], 1);
             s[3] >>= 8;
         };
-        for (int blk = 0; blk < blocks; ++blk) {
-            step(std::integral_constant<int, 0>{}, blk * kBlock8);
-            step(std::integral_constant<int, 1>{}, blk * kBlock8 + kStep8);
-            if ((blk & 15) == 15) {
-                if (blk + 1 < blocks) scales(blk + 1);
-                continue;
+        // (the inner loop has no branch: past one the compiler would sink the
+        // products, and the loads would stand together)
+        for (int b0 = 0; b0 < blocks; b0 += 16) {
+            scales(b0);
+            const int end = min(b0 + 16, blocks);
+            for (int blk = b0; blk < end; ++blk) {
+                step(std::integral_constant<int, 0>{}, blk * kBlock8);
+                step(std::integral_constant<int, 1>{}, blk * kBlock8 + kStep8);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) on(sa[i]);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) on(sb[j]);
             }
-#pragma unroll
-            for (int i = 0; i < FM; ++i) on(sa[i]);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) on(sb[j]);
         }
         // the last steps' loads, past K, still write zeros to LDS
         step_barrier<0>();
     }
 };
 
-// V consecutive results of a row from their sums, with V such that they are 16
-// bytes: bias, activation, and stores of 16 bytes where `wide`
-template <class T, int ACT, int V>
-LS_DEV void put8(const float* v, const T* bias, T* c, int col, int N, bool wide) {
-    struct __attribute__((aligned(16))) TV { T v[V]; } o;
-    if (wide) {  // N is a multiple of 16 bytes: all or nothing
-        if (col >= N) return;
-        TV b = {};
-        if (bias) b = *(const TV*)(bias + col);
+typedef uint32_t Words8 __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any element
+
+// 16 columns' bias from column col, zeros past N
+template <class T>
+LS_DEV void bias16(float (&o)[16], const T* bias, int col, int N) {
+    constexpr int V = 16 / (int)sizeof(T);
 #pragma unroll
-        for (int r = 0; r < V; ++r) o.v[r] = from_f<T>(act_of<ACT, T>(v[r] + (bias ? to_f(b.v[r]) : 0.0f)));
-        *(TV*)(c + col) = o;
-        return;
+    for (int q = 0; q < 16; q += V) {
+        struct { T v[V]; } b = {};
+        if (bias && col + q + V <= N) {
+            b = __builtin_bit_cast(decltype(b), *reinterpret_cast<const Words8*>(bias + col + q));
+        } else if (bias) {
+#pragma unroll
+            for (int r = 0; r < V; ++r)
+                if (col + q + r < N) b.v[r] = bias[col + q + r];
+        }
+#pragma unroll
+        for (int r = 0; r < V; ++r) o[q + r] = to_f(b.v[r]);
     }
+}
+// 16 results of a row, as 16-byte stores at any element's address
+template <class T, int ACT>
+LS_DEV void put16(const f32x16& v, const float (&b)[16], T* c, int col, int N) {
+    constexpr int V = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int r = 0; r < V; ++r)
-        if (col + r < N) c[col + r] = from_f<T>(act_of<ACT, T>(v[r] + (bias ? to_f(bias[col + r]) : 0.0f)));
+    for (int q = 0; q < 16; q += V) {
+        struct { T v[V]; } o;
+#pragma unroll
+        for (int r = 0; r < V; ++r) o.v[r] = from_f<T>(act_of<ACT, T>(v[q + r] + b[q + r]));
+        if (col + q + V <= N) {
+            *reinterpret_cast<Words8*>(c + col + q) = __builtin_bit_cast(u32x4, o);
+        } else {
+#pragma unroll
+            for (int r = 0; r < V; ++r)
+                if (col + q + r < N) c[col + q + r] = o.v[r];
+        }
+    }
 }
 
 struct Piece8 {
@@ -273,7 +297,6 @@ struct Piece8 {
     const void* bias;
     void* c;
     int M, N, blocks;  // blocks: 0 for unused rows
-    bool wide;
 };
 template <class T, int ACT, int BM, int BN>
 LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
@@ -287,26 +310,22 @@ LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
     }
     const int l = lane_id(), w = uniform(threadIdx.x >> 6);
     const int r0 = (w >> 1) * (BM / 2), c0 = (w & 1) * (BN / 2);
-    constexpr int V = 16 / (int)sizeof(T);
     const T* bias = p.bias ? (const T*)p.bias + j0 : nullptr;
 #pragma unroll
-    for (int i = 0; i < Tile::FM; ++i) {
-        const int row = r0 + i * 32 + (l & 31);
-        if (row >= M) continue;
-        T* c = (T*)p.c + (long long)(i0 + row) * p.N + j0;
+    for (int j = 0; j < Tile::FN; ++j) {
+        const int col = c0 + j * 32 + (l >> 5) * 16;
+        float b[16];
+        bias16<T>(b, bias, col, N);
 #pragma unroll
-        for (int j = 0; j < Tile::FN; ++j) {
-            float v[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) v[r] = tile.acc[i][j][r];
-#pragma unroll
-            for (int q = 0; q < 16; q += V) put8<T, ACT, V>(v + q, bias, c, c0 + j * 32 + (l >> 5) * 16 + q, N, p.wide);
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = r0 + i * 32 + (l & 31);
+            if (row < M) put16<T, ACT>(tile.acc[i][j], b, (T*)p.c + (long long)(i0 + row) * p.N + j0, col, N);
         }
     }
 }
 
 template <class T, int ACT, int B>
-__global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g, bool wide) {
+__global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g) {
     constexpr int kGroup = 4;  // row tiles that walk the columns together
     constexpr bool kCut = B == 256;
     __shared__ __align__(1024) char lds[TileSums8<B, B, false>::kLds];
@@ -329,7 +348,6 @@ __global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g, bool
     p.left_b = (g.E - e) * mat;
     p.bias = g.bias && used ? (const T*)g.bias + e * g.out : nullptr;
     p.c = (T*)g.c + (long long)at.elo * g.out;
-    p.wide = wide;
     const int q = t.tile - at.first * cols, tiles = (p.M + B - 1) / B;
     const int first = q / (kGroup * cols) * kGroup, n = min(kGroup, tiles - first), in = q - first * cols;
     int i0 = (first + in % n) * B, j0 = in / n * B;
@@ -346,7 +364,6 @@ __global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g, bool
 
 void launch_expert_linear8(int dtype, const Linear8Args& g, hipStream_t st) {
     if (g.P < 1 || g.out < 1) return;
-    const bool wide = (long long)g.out * (long long)dtype_size(dtype) % 16 == 0 && aligned16(g.c) && aligned16(g.bias);
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
         with_act(g.act, [&](auto av) {
@@ -354,7 +371,7 @@ void launch_expert_linear8(int dtype, const Linear8Args& g, hipStream_t st) {
                 constexpr int B = bv.value;
                 const long long tiles = max_row_tiles<B>(g.P, g.E) * ceil_div(g.out, B);
                 hipLaunchKernelGGL((k_linear8<T, decltype(av)::value, B>), dim3((unsigned)turns(tiles, B == 256)),
-                                   dim3(kProductThreads), 0, st, g, wide);
+                                   dim3(kProductThreads), 0, st, g);
             };
             const long long per = g.P / g.E;
             // one tile a workgroup, whose threads a launch counts in 32 bits

@@ -18,6 +18,11 @@
 //
 // Statistics, sums and partial sums are fp32.  The row's own rounding to 16
 // bits happens once, at the store.
+//
+// Memory bounds it: 16384 rows of 4096 in bf16 with fp32 weights, 268 MB, 55 us
+// (4.9 TB/s); its gradients, 403 MB, 77 us (5.2 TB/s) of which k_norm_sum is 7.
+// 1000 rows of 1001 in fp32: 4.7 and 10 us, latencies of a row's loads and of the
+// sums after each other.
 #include "lapsum_layer_ops.h"
 #include "lapsum_rows.h"
 
@@ -79,11 +84,29 @@ LS_DEV void row_moments(float& mean, float& sq, float n, float D, float (*s)[2][
 }
 
 // V elements from column c of a row of D weights, as floats; `none` where
-// there are none
+// there are none.  (One load an element instead of 16 bytes: 16384 rows of 4096
+// with fp32 weights 69 us in place of 59, its gradients 84 in place of 77.)
 template <class W, int V>
 LS_DEV void weights(float (&v)[V], const W* __restrict__ w, long long c, long long D, float none) {
+    constexpr int P = V < Pack<W>::V ? V : Pack<W>::V;
+    struct __attribute__((packed, aligned(sizeof(W)))) Few {
+        W v[P];
+    };
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = w && c + i < D ? to_f(w[c + i]) : none;
+    for (int i = 0; i < V; ++i) v[i] = none;
+    if (!w) return;
+#pragma unroll
+    for (int p = 0; p < V; p += P) {
+        if (c + p + P <= D) {
+            const Few x = *reinterpret_cast<const Few*>(w + c + p);
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[p + i] = to_f(x.v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (c + p + i < D) v[p + i] = to_f(w[c + p + i]);
+        }
+    }
 }
 
 template <class T, class W, int NT, int U>
@@ -103,6 +126,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* __restric
         weights<W, V>(b[u], bias, c, D, 0.0f);
         mine += (int)min(max(D - c, 0ll), (long long)V);
     }
+    const int held = mine;
     const float n = wave_sum_f32((float)mine), inv = 1.0f / fmaxf(n, 1.0f);
     int flip = 0;
     Pack<T> next[U];
@@ -110,15 +134,17 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* __restric
     long long r = (long long)blockIdx.x * kRows + sub;
     auto load = [&](long long row) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = ld<false>(x + row * D, (long long)(u * NT + tid) * V, D);
+        for (int u = 0; u < U; ++u) next[u] = take<false>(x + row * D, (long long)(u * NT + tid) * V, D);
     };
     if (r < rows) load(r);
     for (; r < rows; r += stride) {
         float v[U][V];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            const Pack<T> p = settle(next[u], (long long)(u * NT + tid) * V, D);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[u][i] = to_f(next[u].v[i]);
+            for (int i = 0; i < V; ++i) v[u][i] = to_f(p.v[i]);
+        }
         if (r + stride < rows) load(r + stride);
         float sum = 0.0f;  // (past the row's end the packs hold zeros)
 #pragma unroll
@@ -128,12 +154,21 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* __restric
         float mean = wave_sum_f32(sum) * inv, sq = 0.0f, left = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long c = (long long)(u * NT + tid) * V;
+            const int n_u = min(max(held - u * V, 0), V);
+            if (n_u == V) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = c + i < D ? v[u][i] - mean : 0.0f;
-                sq = fmaf(d, d, sq);
-                left += d;
+                for (int i = 0; i < V; ++i) {
+                    const float d = v[u][i] - mean;
+                    sq = fmaf(d, d, sq);
+                    left += d;
+                }
+            } else {  // the row's end
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = i < n_u ? v[u][i] - mean : 0.0f;
+                    sq = fmaf(d, d, sq);
+                    left += d;
+                }
             }
         }
         left = wave_sum_f32(left);
@@ -218,8 +253,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_vjp(const T* __res
     __shared__ float meet[kRows > 1 ? kRows : 1][kRows > 1 ? NT * V : 1];
     const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
     float w[U][V], dw[U][V] = {}, db[U][V] = {};
+    auto load_weights = [&] {
 #pragma unroll
-    for (int u = 0; u < U; ++u) weights<W, V>(w[u], weight, (long long)(u * NT + tid) * V, D, 1.0f);
+        for (int u = 0; u < U; ++u) weights<W, V>(w[u], weight, (long long)(u * NT + tid) * V, D, 1.0f);
+    };
     const float inv = 1.0f / (float)D;
     int flip = 0;
     Pack<T> nx[U], ng[U];
@@ -231,29 +268,37 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_vjp(const T* __res
         ns = rstd_in[row];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            nx[u] = ld<true>(x + row * D, (long long)(u * NT + tid) * V, D);
-            ng[u] = ld<true>(dy + row * D, (long long)(u * NT + tid) * V, D);
+            nx[u] = take<true>(x + row * D, (long long)(u * NT + tid) * V, D);
+            ng[u] = take<true>(dy + row * D, (long long)(u * NT + tid) * V, D);
         }
     };
-    if (r < rows) load(r);
+    // the widest rows leave no registers for the next one's and for weights
+    // (4096 rows of 16384 in bf16: 150 us with both, 119 with neither)
+    constexpr bool kAhead = U < 4;
+    if (kAhead) load_weights();
+    if (kAhead && r < rows) load(r);
     for (; r < rows; r += stride) {
+        if (!kAhead) load(r), load_weights();
         float xh[U][V], g[U][V];
         const float mean = nm, rstd = ns;
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            const long long c = (long long)(u * NT + tid) * V;
+            const Pack<T> px = settle(nx[u], c, D), pg = settle(ng[u], c, D);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 // (past the row's end dy is 0)
-                xh[u][i] = (to_f(nx[u].v[i]) - mean) * rstd;
-                const float d = to_f(ng[u].v[i]);
+                xh[u][i] = (to_f(px.v[i]) - mean) * rstd;
+                const float d = to_f(pg.v[i]);
                 dw[u][i] = fmaf(d, xh[u][i], dw[u][i]);
                 db[u][i] += d;
                 g[u][i] = d * w[u][i];
                 s1 += g[u][i];
                 s2 = fmaf(g[u][i], xh[u][i], s2);
             }
-        if (r + stride < rows) load(r + stride);
+        }
+        if (kAhead && r + stride < rows) load(r + stride);
         if (!dx) continue;
         row_sums<NT>(s1, s2, s, flip);
         s1 *= inv;
@@ -286,8 +331,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_vjp(const T* __res
             }
             const long long c = (long long)(u * NT + tid) * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (c + i < D) to[c + i] = a[i];
+            for (int p = 0; p < V; p += 4) {
+                const Pack<float> o{{a[p], a[p + 1], a[p + 2], a[p + 3]}};
+                st<float>(to, c + p, D, o);
+            }
         }
     }
 }
@@ -355,12 +402,12 @@ __global__ __launch_bounds__(256) void k_norm_dw_wide(const T* __restrict__ x, c
 }
 
 // dw (blockIdx.y = 0) and db from their n partial rows, 64 columns a
-// workgroup: a wave adds every fourth row, and the waves' sums are added in
+// workgroup: a wave adds every sixteenth row, and the waves' sums are added in
 // wave order
 template <class W>
-__global__ __launch_bounds__(256) void k_norm_sum(const float* __restrict__ part, int n, long long D,
-                                                  W* __restrict__ dw, W* __restrict__ db) {
-    __shared__ float s[4][64];
+__global__ __launch_bounds__(1024) void k_norm_sum(const float* __restrict__ part, int n, long long D,
+                                                   W* __restrict__ dw, W* __restrict__ db) {
+    __shared__ float s[16][64];
     W* to = blockIdx.y ? db : dw;
     if (!to) return;
     const float* p = part + (long long)blockIdx.y * n * D;
@@ -370,11 +417,15 @@ __global__ __launch_bounds__(256) void k_norm_sum(const float* __restrict__ part
         float sum = 0.0f;
         if (c < D) {
 #pragma unroll 8
-            for (int i = w; i < n; i += 4) sum += p[(long long)i * D + c];
+            for (int i = w; i < n; i += 16) sum += p[(long long)i * D + c];
         }
         s[w][l] = sum;
         __syncthreads();
-        if (w == 0 && c < D) to[c] = from_f<W>((s[0][l] + s[1][l]) + (s[2][l] + s[3][l]));
+        if (w == 0 && c < D) {
+#pragma unroll
+            for (int i = 1; i < 16; ++i) sum += s[i][l];
+            to[c] = from_f<W>(sum);
+        }
         __syncthreads();
     }
 }
@@ -421,7 +472,11 @@ void launch_norm(const void* x, const void* weight, const void* bias, int dtype,
                                    (const W*)weight, (const W*)bias, rows, D, eps, (T*)y, mean, rstd);
             } else {
                 constexpr int kRows = NT < 256 ? 256 / NT : 1;
-                const long long groups = std::min<long long>(ceil_div(rows, kRows), 256 * 2048 / std::max(NT, 256));
+                // the workgroups that are resident at once, or nearly (16384 rows
+                // of 4096 in bf16, two / four / five / eight on a CU: 60 / 55 / 66
+                // / 62 us; 8192 of 8192, one / two of 512 threads: 63 / 52)
+                constexpr long long kMost = NT <= 256 ? 1024 : U < 4 ? 512 : 256;
+                const long long groups = std::min<long long>(ceil_div(rows, kRows), kMost);
                 hipLaunchKernelGGL((k_norm<T, W, NT, U>), dim3((unsigned)groups), dim3(std::max(NT, 256)), 0, st,
                                    (const T*)x, (const W*)weight, (const W*)bias, rows, D, eps, (T*)y, mean, rstd);
             }
@@ -436,8 +491,11 @@ static long long norm_parts(int dtype, long long rows, long long D) {
         using T = decltype(tv);
         with_shape<T>(D, [&](auto nt, auto) {
             constexpr int NT = nt.value;
+            // a workgroup's partial row is written and read again: two of 256
+            // threads on a CU (16384 rows of 4096 in bf16, one / two / four: 81 / 77
+            // / 88 us; 65536 of 1024: 78 / 75 / 88), or one of 512
             if constexpr (NT == 0) n = std::min<long long>(rows, 64);
-            else n = std::min<long long>(ceil_div(rows, NT < 256 ? 256 / NT : 1), 256 * 1024 / std::max(NT, 256));
+            else n = std::min<long long>(ceil_div(rows, NT < 256 ? 256 / NT : 1), 256 * 512 / std::max(NT, 256));
         });
     });
     return std::max(n, 1ll);
@@ -469,7 +527,7 @@ void launch_norm_vjp(const void* x, const void* weight, const float* mean, const
             }
         });
         if (part)
-            hipLaunchKernelGGL((k_norm_sum<W>), dim3(grid_of(ceil_div(D, 64)), 2), dim3(256), 0, st, part, (int)n, D,
+            hipLaunchKernelGGL((k_norm_sum<W>), dim3(grid_of(ceil_div(D, 64)), 2), dim3(1024), 0, st, part, (int)n, D,
                                (W*)dweight, (W*)dbias);
     });
 }

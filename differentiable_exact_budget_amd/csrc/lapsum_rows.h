@@ -36,6 +36,30 @@ LS_DEV Pack<T> ld(const T* row, long long c, long long D) {
     }
     return x;
 }
+// The same in two steps, for loads that are to stay in flight: at a row's end
+// take() brings the row's last 16 bytes, and settle() shifts them down (D as
+// above, and the elements past it zero).  A row's last elements loaded one by
+// one, or shifted at once, make every load wait for those before it: layer norm's
+// gradients of 32768 rows of 300 in bf16 43 and 33 us, 25 so.
+template <bool ONCE, class T>
+LS_DEV Pack<T> take(const T* row, long long c, long long D) {
+    constexpr int V = Pack<T>::V;
+    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+    if (D < V) return ld<ONCE>(row, c, D);
+    const T* p = row + min(c, D - V);
+    if (ONCE) return __builtin_bit_cast(Pack<T>, __builtin_nontemporal_load(reinterpret_cast<const Words*>(p)));
+    return reinterpret_cast<const Loose<T>*>(p)->p;
+}
+template <class T>
+LS_DEV Pack<T> settle(const Pack<T>& x, long long c, long long D) {
+    constexpr int V = Pack<T>::V;
+    if (D < V || c + V <= D) return x;
+    struct { uint64_t lo, hi; } w = __builtin_bit_cast(decltype(w), x);
+    const int by = (int)min(c - (D - V), (long long)V) * 8 * (int)sizeof(T);  // 16 .. 128
+    w.lo = by >= 128 ? 0 : by >= 64 ? w.hi >> (by - 64) : w.lo >> by | w.hi << (64 - by);
+    w.hi = by >= 64 ? 0 : w.hi >> by;
+    return __builtin_bit_cast(Pack<T>, w);
+}
 template <class T>
 LS_DEV void st(T* row, long long c, long long D, const Pack<T>& x) {
     constexpr int V = Pack<T>::V;
