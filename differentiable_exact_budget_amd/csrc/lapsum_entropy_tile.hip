@@ -56,10 +56,14 @@ LS_DEV TileAt tile_at(int rows, int cols, bool cut) {
 
 // ---- forward ---------------------------------------------------------------------
 
+// Up to kFewRows rows a tile's own loads would leave most of it empty; few_tile
+// streams the weights instead (NNN).
+constexpr int kFewRows = 64, kFewCols = 64, kFewWaves = 4;
+
 LossParts loss_tile_parts(const LossArgs& g) {
     LossParts p{};
     const int side = side_of(g.T, g.V);
-    p.parts = 2 * (int)ceil_div(g.V, side);
+    p.parts = (int)(g.T <= kFewRows ? ceil_div(g.V, kFewCols) : 2 * ceil_div(g.V, side));
     size_t at = 0;
     p.pairs = take(at, (size_t)p.parts * g.T * sizeof(float2));
     p.zt = take(at, (size_t)g.T * 4);
@@ -151,7 +155,115 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int r
     }
 }
 
+// 16 FM rows and kFewCols columns: bound by reading the weights, once.  The
+// waves split the sum; each multiplies its share straight from memory (a weight
+// is used once, so LDS would only add a stop on its way), and their sums meet in
+// LDS, added in wave order.
+template <class T, int FM>
+__global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, float2* __restrict__ pairs,
+                                                              float* __restrict__ zt) {
+    constexpr int FN = kFewCols / 16, U = FM == 1 ? 4 : 2;  // steps of 32 k in flight
+    constexpr int kPad = kFewCols + 4;
+    __shared__ float part[kFewWaves][16][kPad];
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6), i16 = l & 15, k8 = (l >> 4) * 8;
+    const int j0 = blockIdx.x * kFewCols, D = g.D;
+    // this lane's rows: those past the end read the last one again, and their
+    // results are not stored
+    const T *x[FM], *b[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) x[i] = (const T*)g.x + (long long)min(i * 16 + i16, g.T - 1) * D + k8;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b[j] = (const T*)g.w + (long long)min(j0 + j * 16 + i16, g.V - 1) * D + k8;
+    f32x4 acc[FM][FN] = {};
+    const int steps = (D + 31) / 32, whole = D / 32, s1 = (w + 1) * steps / kFewWaves;
+    int s = w * steps / kFewWaves;
+    for (; s + U <= min(s1, whole); s += U) {
+        s16x8 fx[U][FM], fb[U][FN];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) fb[u][j] = *(const s16x8*)(b[j] + (s + u) * 32);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) fx[u][i] = *(const s16x8*)(x[i] + (s + u) * 32);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<T>(fb[u][j], fx[u][i], acc[i][j]);
+    }
+    for (; s < s1; ++s) {
+        const bool on = s * 32 + k8 < D;
+        s16x8 fx[FM], fb[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = on ? *(const s16x8*)(b[j] + s * 32) : s16x8{};
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fx[i] = on ? *(const s16x8*)(x[i] + s * 32) : s16x8{};
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<T>(fb[j], fx[i], acc[i][j]);
+    }
+    // lane l holds row l % 16 of a fragment, columns 4 (l / 16) .. + 3
+    const int row = threadIdx.x >> 4, c = (threadIdx.x & 15) * 4;
+    float add[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        add[r] = j0 + c + r >= g.V ? -__builtin_inff() : g.bias ? to_f(((const T*)g.bias)[j0 + c + r]) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        if (i) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < FN; ++j) *(f32x4*)&part[w][i16][j * 16 + (l >> 4) * 4] = acc[i][j];
+        __syncthreads();
+        const int t = i * 16 + row;
+        if (t >= g.T) continue;  // (all 16 lanes of a row)
+        f32x4 v = *(const f32x4*)&part[0][row][c];
+#pragma unroll
+        for (int p = 1; p < kFewWaves; ++p) v += *(const f32x4*)&part[p][row][c];
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            v[r] += add[r];
+            m = fmaxf(m, v[r]);
+        }
+        m = fmaxf(m, __uint_as_float(xor_lane<8>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<4>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<2>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<1>(__float_as_uint(m))));
+        const float from = m == -__builtin_inff() ? 0.0f : m * -kLog2e;
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f(fmaf(v[r], kLog2e, from));
+        sum += __uint_as_float(xor_lane<8>(__float_as_uint(sum)));
+        sum += __uint_as_float(xor_lane<4>(__float_as_uint(sum)));
+        sum += __uint_as_float(xor_lane<2>(__float_as_uint(sum)));
+        sum += __uint_as_float(xor_lane<1>(__float_as_uint(sum)));
+        if (c == 0) pairs[(long long)blockIdx.x * g.T + t] = make_float2(m, sum);
+        const int64_t target = g.target[t], at = target - j0 - c;
+        if (target < 0 || target >= g.V || at < 0 || at >= 4) continue;
+        zt[t] = at == 0 ? v[0] : at == 1 ? v[1] : at == 2 ? v[2] : v[3];
+    }
+}
+
 void launch_loss_tile(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st) {
+    if (g.T <= kFewRows) {
+        with_dtype(dtype, [&](auto tv) {
+            using T = decltype(tv);
+            if constexpr (sizeof(T) == 2) {
+                auto launch = [&](auto fm) {
+                    hipLaunchKernelGGL((k_loss_few<T, fm.value>), dim3((unsigned)ceil_div(g.V, kFewCols)),
+                                       dim3(kFewWaves * 64), 0, st, g, (float2*)(scratch + p.pairs),
+                                       (float*)(scratch + p.zt));
+                };
+                if (g.T <= 16) launch(std::integral_constant<int, 1>{});
+                else if (g.T <= 32) launch(std::integral_constant<int, 2>{});
+                else launch(std::integral_constant<int, 4>{});
+            }
+        });
+        return;
+    }
     with_side(side_of(g.T, g.V), [&](auto bv) {
         constexpr int B = bv.value;
         const long long rows = ceil_div(g.T, B), cols = ceil_div(g.V, B);
@@ -220,12 +332,19 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_dtile(LossArgs g, int 
         for (int i = 0; i < Tile::FM; ++i) {
             const int row = r0 + i * 16 + (l & 15);
             T8 o;
+            float p[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const float v = tile.acc[i][j + (r >> 2)][r & 3] + b[r];
-                const float p = __builtin_amdgcn_exp2f(fmaf(v, kLog2e, lo[i])) - (hit[i] == in + r ? 1.0f : 0.0f);
+                float v = tile.acc[i][j + (r >> 2)][r & 3];
+                if (bias) v += b[r];
+                p[r] = __builtin_amdgcn_exp2f(fmaf(v, kLog2e, lo[i]));
                 // an ignored row has no gradient, whatever its logits are
-                o.v[r] = from_f<T>(gt[i] == 0.0f ? 0.0f : p * gt[i]);
+                o.v[r] = from_f<T>(gt[i] == 0.0f ? 0.0f : p[r] * gt[i]);
+            }
+            if ((hit[i] & ~7) == in && gt[i] != 0.0f) {  // the target is here
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (hit[i] == in + r) o.v[r] = from_f<T>((p[r] - 1.0f) * gt[i]);
             }
             if (col + 8 > N) {
 #pragma unroll

@@ -254,43 +254,6 @@ struct TileSums8 {
 
 typedef uint32_t Words8 __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any element
 
-// 16 columns' bias from column col, zeros past N
-template <class T>
-LS_DEV void bias16(float (&o)[16], const T* bias, int col, int N) {
-    constexpr int V = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int q = 0; q < 16; q += V) {
-        struct { T v[V]; } b = {};
-        if (bias && col + q + V <= N) {
-            b = __builtin_bit_cast(decltype(b), *reinterpret_cast<const Words8*>(bias + col + q));
-        } else if (bias) {
-#pragma unroll
-            for (int r = 0; r < V; ++r)
-                if (col + q + r < N) b.v[r] = bias[col + q + r];
-        }
-#pragma unroll
-        for (int r = 0; r < V; ++r) o[q + r] = to_f(b.v[r]);
-    }
-}
-// 16 results of a row, as 16-byte stores at any element's address
-template <class T, int ACT>
-LS_DEV void put16(const f32x16& v, const float (&b)[16], T* c, int col, int N) {
-    constexpr int V = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int q = 0; q < 16; q += V) {
-        struct { T v[V]; } o;
-#pragma unroll
-        for (int r = 0; r < V; ++r) o.v[r] = from_f<T>(act_of<ACT, T>(v[q + r] + b[q + r]));
-        if (col + q + V <= N) {
-            *reinterpret_cast<Words8*>(c + col + q) = __builtin_bit_cast(u32x4, o);
-        } else {
-#pragma unroll
-            for (int r = 0; r < V; ++r)
-                if (col + q + r < N) c[col + q + r] = o.v[r];
-        }
-    }
-}
-
 struct Piece8 {
     const uint8_t *a, *as, *b, *bs;
     long long left_a, left_b;
@@ -308,18 +271,65 @@ LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
         tile.run(p.a + a * kBlock8, p.as + a, M, p.left_a - a, p.b + b * kBlock8, p.bs + b, N, p.left_b - b, p.blocks,
                  lds);
     }
+    // A wave's quarter leaves through its own part of LDS, kPass rows at a time:
+    // in registers a lane has 16 columns of 32 rows, from LDS it takes 16 bytes
+    // of a row, its neighbours the next, so bias and activation are a short loop
+    // and the stores are whole lines (unrolled over the registers: the same time
+    // from ten times the code).
+    constexpr int WR = BM / 2, WC = BN / 2, V = 16 / (int)sizeof(T);
+    constexpr int kLine = WC * 4 + 16;  // bytes of a row: neighbouring rows meet other banks
+    constexpr int kPass = WR < 64 ? WR : 64;
+    static_assert(4 * kPass * kLine <= Tile::kLds);
+    constexpr int kLanes = WC / V, kRows = 64 / kLanes;  // lanes of a row, rows at a time
     const int l = lane_id(), w = uniform(threadIdx.x >> 6);
-    const int r0 = (w >> 1) * (BM / 2), c0 = (w & 1) * (BN / 2);
-    const T* bias = p.bias ? (const T*)p.bias + j0 : nullptr;
+    const int r0 = i0 + (w >> 1) * WR, c0 = j0 + (w & 1) * WC;
+    const int col = c0 + l % kLanes * V;
+    char* own = lds + w * kPass * kLine;
+    struct Chunk { T v[V]; };
+    Chunk bias{};
+    const bool whole = col + V <= p.N;
+    if (p.bias && whole) {
+        bias = __builtin_bit_cast(Chunk, *reinterpret_cast<const Words8*>((const T*)p.bias + col));
+    } else if (p.bias) {
 #pragma unroll
-    for (int j = 0; j < Tile::FN; ++j) {
-        const int col = c0 + j * 32 + (l >> 5) * 16;
-        float b[16];
-        bias16<T>(b, bias, col, N);
+        for (int r = 0; r < V; ++r)
+            if (col + r < p.N) bias.v[r] = ((const T*)p.bias)[col + r];
+    }
 #pragma unroll
-        for (int i = 0; i < Tile::FM; ++i) {
-            const int row = r0 + i * 32 + (l & 31);
-            if (row < M) put16<T, ACT>(tile.acc[i][j], b, (T*)p.c + (long long)(i0 + row) * p.N + j0, col, N);
+    for (int pass = 0; pass < WR; pass += kPass) {
+        // (a wave's own LDS operations are served in order)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < kPass / 32; ++i)
+#pragma unroll
+            for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    const f32x16& a = tile.acc[pass / 32 + i][j];
+                    *(f32x4*)(own + (i * 32 + (l & 31)) * kLine + (j * 32 + (l >> 5) * 16 + q) * 4) =
+                        f32x4{a[q], a[q + 1], a[q + 2], a[q + 3]};
+                }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 2
+        for (int r = l / kLanes; r < kPass; r += kRows) {
+            const int row = r0 + pass + r;
+            const f32x4* at = (const f32x4*)(own + r * kLine + l % kLanes * V * 4);
+            Chunk o;
+#pragma unroll
+            for (int q = 0; q < V; q += 4) {
+                const f32x4 v = at[q / 4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o.v[q + e] = from_f<T>(act_of<ACT, T>(v[e] + to_f(bias.v[q + e])));
+            }
+            if (row >= p.M) continue;
+            T* c = (T*)p.c + (long long)row * p.N + col;
+            if (whole) {
+                *reinterpret_cast<Words8*>(c) = __builtin_bit_cast(u32x4, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (col + e < p.N) c[e] = o.v[e];
+            }
         }
     }
 }
