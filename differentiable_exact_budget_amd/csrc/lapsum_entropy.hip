@@ -10,8 +10,9 @@
 // merges.  Backward, z is formed again, a piece of the vocabulary at a time,
 // and turned into d by the lse of the forward pass.
 //
-// Here pieces of z are formed in fp32 in scratch by the products for any
-// alignment (lapsum_tile_any.h) and read from there.  d is rounded to the rows'
+// Here the products are those for any alignment (lapsum_tile_any.h).  Tiles of
+// 32 columns reduce them as they are; wide tiles' logits go through scratch in
+// fp32, a piece of the vocabulary at a time.  d is rounded to the rows'
 // type once, because the matrix instructions take it so; for fp16, whose range
 // ends at 6e-8, d is scaled by a power of two that brings the largest gradient
 // of a row's loss to 2^13 .. 2^14, and the products are scaled back in fp32.
@@ -21,7 +22,7 @@
 namespace lapsum {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr long long kPieceBytes = 128ll << 20;  // of fp32 logits
+constexpr long long kPieceBytes = 128ll << 20;  // of fp32 logits, or of d as it were fp32
 static_assert(sizeof(float2) == 8);
 
 static size_t take(size_t& at, size_t bytes) {
@@ -30,20 +31,28 @@ static size_t take(size_t& at, size_t bytes) {
     return here;
 }
 
+// As for the experts' products: 128 x 128 tiles where there are enough and rows to
+// fill them, else 32 x 32 with the sum shared by the waves.
+static bool wide_tiles(int dtype, long long M, long long N, int shares) {
+    return std::min(M, N) > 64 && ceil_div(N, 128) * ceil_div(M, 128) * shares >= (dtype == kF32 ? 384 : 128);
+}
+
 static int any_width(const LossArgs& g) {
     const long long w = std::max(kPieceBytes / 4 / std::max(g.T, 1) / 128 * 128, 128ll);
     return (int)std::min<long long>(w, std::max(g.V, 1));
 }
 
-LossParts loss_any_parts(const LossArgs& g) {
+LossParts loss_any_parts(int dtype, const LossArgs& g) {
     LossParts p{};
     p.width = any_width(g);
-    p.parts = (int)ceil_div(g.V, p.width);
+    // narrow tiles reduce their columns themselves
+    const bool logits = wide_tiles(dtype, g.T, std::min(p.width, g.V), 1);
+    p.parts = (int)(logits ? ceil_div(g.V, p.width) : ceil_div(g.V, 32));
     size_t at = 0;
     p.pairs = take(at, (size_t)p.parts * g.T * sizeof(float2));
     p.zt = take(at, (size_t)g.T * 4);
     p.loss = take(at, (size_t)g.T * 4);
-    p.logits = take(at, (size_t)g.T * p.width * 4);
+    if (logits) p.logits = take(at, (size_t)g.T * p.width * 4);
     p.bytes = at;
     return p;
 }
@@ -62,9 +71,7 @@ LossVjpPlan loss_any_plan(int dtype, const LossArgs& g) {
     p.shares = any_shares(g, p.width);
     size_t at = 0;
     p.g = take(at, ((size_t)g.T + 1) * 4);
-    p.logits = take(at, (size_t)g.T * p.width * 4);
-    // fp32: in the logits' place
-    p.d = dtype == kF32 ? p.logits : take(at, (size_t)g.T * p.width * dtype_size(dtype));
+    p.d = take(at, (size_t)g.T * p.width * dtype_size(dtype));
     if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
     p.bytes = at;
     return p;
@@ -78,6 +85,51 @@ struct PutLogits {
     const T* bias;
     long long ldc;
     LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = bias ? v + to_f(bias[j]) : v; }
+};
+// a row's pair of the tile's columns, and the target's logit
+template <class T>
+struct PutPairs {
+    const T* bias;
+    const int64_t* target;  // of the tile's first row
+    long long j0;           // of its first column in the vocabulary
+    int V;
+    float2* pairs;          // of the tile's first row
+    float* zt;
+    LS_DEV void cell(int i, int j, float v, bool on) const {
+        const float z = !on ? -__builtin_inff() : bias ? v + to_f(bias[j]) : v;
+        float m = z;
+        m = fmaxf(m, __uint_as_float(xor_lane<16>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<8>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<4>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<2>(__float_as_uint(m))));
+        m = fmaxf(m, __uint_as_float(xor_lane<1>(__float_as_uint(m))));
+        const float from = m == -__builtin_inff() ? 0.0f : m;
+        float s = __builtin_amdgcn_exp2f((z - from) * kLog2e);
+        s += __uint_as_float(xor_lane<16>(__float_as_uint(s)));
+        s += __uint_as_float(xor_lane<8>(__float_as_uint(s)));
+        s += __uint_as_float(xor_lane<4>(__float_as_uint(s)));
+        s += __uint_as_float(xor_lane<2>(__float_as_uint(s)));
+        s += __uint_as_float(xor_lane<1>(__float_as_uint(s)));
+        if (!on) return;
+        if (j == 0) pairs[i] = make_float2(m, s);
+        if (target[i] == j0 + j) zt[i] = z;
+    }
+    LS_DEV void one(int, int, float) const {}
+};
+// d of a piece
+template <class T>
+struct PutD {
+    T* d;
+    const T* bias;
+    const int64_t* target;  // of the tile's first row
+    const float *lse, *g;
+    long long ld, j0;
+    LS_DEV void one(int i, int j, float v) const {
+        const float z = bias ? v + to_f(bias[j]) : v, gt = g[i];
+        const float p = __builtin_amdgcn_exp2f((z - lse[i]) * kLog2e);
+        // an ignored row has no gradient, whatever its logits are
+        d[i * ld + j] = from_f<T>(gt == 0.0f ? 0.0f : (p - (target[i] == j0 + j ? 1.0f : 0.0f)) * gt);
+    }
 };
 struct PutPart {
     float* c;
@@ -108,42 +160,56 @@ struct AnyProduct {
     int M, N, K, lda, ldb;
     void* c;
     long long ldc;
-    const void* bias;      // kFormY
-    const float* unscale;  // outputs
+    const float* unscale;  // of rows
     int shares;            // of K: partial sums, M * N elements apart
     bool add;
+    // of logits
+    const void* bias;
+    const int64_t* target;
+    const float *lse, *g;
+    int v0, V;             // the piece's first column; the vocabulary
+    float2* pairs;
+    float* zt;
 };
-// FORM kFormY: fp32 logits; kFormDx: partial sums (PART) or rows; kFormDw: rows
-template <class T, int FORM, bool PART, int B, bool SPLIT>
+// What becomes of a product's sums: fp32 logits, pairs of the tile's columns, d;
+// partial sums (of dx) or rows (of dx, of dW).
+enum Use : int { kLogits, kPairs, kD, kPartDx, kDx, kDw };
+
+template <class T, int USE, int B, bool SPLIT>
 __global__ __launch_bounds__(kAnyThreads) void k_loss_any(AnyProduct g, long long tiles, int cols) {
-    constexpr bool kA = FORM != kFormDw, kB = FORM == kFormY;
+    constexpr bool kA = USE != kDw, kB = USE <= kD;
     __shared__ __align__(128) char lds[2 * any_steps(SPLIT) * 2 * B * 64 * (SPLIT ? 4 : 1)];
     for (long long t = blockIdx.x; t < tiles * g.shares; t += gridDim.x) {
         const int share = (int)(t / tiles);
         const long long q = t % tiles;
-        const int i0 = (int)(q / cols) * B, j0 = (int)(q % cols) * B;
+        const int i0 = (int)(q / cols) * B, tj = (int)(q % cols), j0 = tj * B;
         const int k0 = (int)((long long)g.K * share / g.shares), k1 = (int)((long long)g.K * (share + 1) / g.shares);
         const T* a = (const T*)g.a + (kA ? (long long)i0 * g.lda + k0 : (long long)k0 * g.lda + i0);
         const T* b = (const T*)g.b + (kB ? (long long)j0 * g.ldb + k0 : (long long)k0 * g.ldb + j0);
+        const T* bias = g.bias ? (const T*)g.bias + j0 : nullptr;
+        const int64_t* target = g.target + i0;
+        const long long to = (long long)i0 * g.ldc + j0, v0 = (long long)g.v0 + j0;
         auto sums = [&](const auto& put) {
             any_sums<T, kA, kB, B, SPLIT>(a, g.M - i0, g.lda, b, g.N - j0, g.ldb, k1 - k0, lds, put);
         };
-        const long long to = (long long)i0 * g.ldc + j0;
-        if constexpr (FORM == kFormY) {
-            Each<PutLogits<T>> put{{(float*)g.c + to, g.bias ? (const T*)g.bias + j0 : nullptr, g.ldc}, g.N - j0};
-            sums(put);
-        } else if constexpr (PART) {
-            Each<PutPart> put{{(float*)g.c + (long long)share * g.M * g.ldc + to, g.ldc, g.add}, g.N - j0};
-            sums(put);
+        const int N = g.N - j0;
+        if constexpr (USE == kLogits) {
+            sums(Each<PutLogits<T>>{{(float*)g.c + to, bias, g.ldc}, N});
+        } else if constexpr (USE == kPairs) {
+            static_assert(SPLIT && B == 32);
+            sums(Each<PutPairs<T>>{{bias, target, v0, g.V, g.pairs + (long long)tj * g.M + i0, g.zt + i0}, N});
+        } else if constexpr (USE == kD) {
+            sums(Each<PutD<T>>{{(T*)g.c + to, bias, target, g.lse + i0, g.g + i0, g.ldc, v0}, N});
+        } else if constexpr (USE == kPartDx) {
+            sums(Each<PutPart>{{(float*)g.c + (long long)share * g.M * g.ldc + to, g.ldc, g.add}, N});
         } else {
-            Each<PutOut<T>> put{{(T*)g.c + to, g.ldc, *g.unscale}, g.N - j0};
-            sums(put);
+            sums(Each<PutOut<T>>{{(T*)g.c + to, g.ldc, *g.unscale}, N});
         }
         __syncthreads();
     }
 }
 
-template <int FORM, bool PART>
+template <int USE>
 static void launch_any_product(int dtype, const AnyProduct& g, hipStream_t st) {
     if (g.M < 1 || g.N < 1) return;
     with_dtype(dtype, [&](auto tv) {
@@ -151,26 +217,32 @@ static void launch_any_product(int dtype, const AnyProduct& g, hipStream_t st) {
         auto launch = [&](auto bv, auto sv) {
             constexpr int B = bv.value;
             const long long cols = ceil_div(g.N, B), tiles = cols * ceil_div(g.M, B);
-            hipLaunchKernelGGL((k_loss_any<T, FORM, PART, B, sv.value>), dim3(grid_of(tiles * g.shares)),
-                               dim3(kAnyThreads), 0, st, g, tiles, (int)cols);
+            hipLaunchKernelGGL((k_loss_any<T, USE, B, sv.value>), dim3(grid_of(tiles * g.shares)), dim3(kAnyThreads), 0,
+                               st, g, tiles, (int)cols);
         };
-        // as for the experts' products: wide tiles where there are enough
-        const long long tiles = ceil_div(g.N, 128) * ceil_div(g.M, 128) * g.shares;
-        if (tiles >= (sizeof(T) == 2 ? 128 : 384)) launch(std::integral_constant<int, 128>{}, std::false_type{});
-        else launch(std::integral_constant<int, 32>{}, std::true_type{});
+        if constexpr (USE == kPairs) {
+            launch(std::integral_constant<int, 32>{}, std::true_type{});
+        } else {
+            const bool wide = USE == kLogits || wide_tiles(dtype, g.M, g.N, g.shares);
+            if (wide) launch(std::integral_constant<int, 128>{}, std::false_type{});
+            else if constexpr (USE != kLogits) launch(std::integral_constant<int, 32>{}, std::true_type{});
+        }
     });
 }
 
-static void any_logits(int dtype, const LossArgs& g, int v0, int n, int width, float* logits, hipStream_t st) {
+// the product of rows and a piece of the vocabulary
+static AnyProduct any_piece(int dtype, const LossArgs& g, int v0, int n, void* c, long long ldc) {
     const size_t es = dtype_size(dtype);
     AnyProduct p{};
     p.a = g.x;
     p.b = (const char*)g.w + (size_t)v0 * g.D * es;
     p.bias = g.bias ? (const char*)g.bias + (size_t)v0 * es : nullptr;
     p.M = g.T, p.N = n, p.K = g.D, p.lda = g.D, p.ldb = g.D;
-    p.c = logits, p.ldc = width;
+    p.c = c, p.ldc = ldc;
     p.shares = 1;
-    launch_any_product<kFormY, false>(dtype, p, st);
+    p.target = g.target;
+    p.v0 = v0, p.V = g.V;
+    return p;
 }
 
 // ---- rows of logits ---------------------------------------------------------------
@@ -191,7 +263,8 @@ LS_DEV MaxSum merge_lanes(MaxSum a) {
     return merge(a, {__uint_as_float(xor_lane<D>(__float_as_uint(a.m))), __uint_as_float(xor_lane<D>(__float_as_uint(a.s)))});
 }
 
-// a row of a piece, one workgroup: its pair, and the target's logit
+// A row of a piece, one workgroup: its pair, and the target's logit.  The row is
+// read twice, the second time from the caches.
 __global__ __launch_bounds__(256) void k_loss_part(const float* __restrict__ z, const int64_t* __restrict__ target,
                                                    int T, int V, int v0, int n, int ld, float2* __restrict__ pairs,
                                                    float* __restrict__ zt) {
@@ -199,7 +272,11 @@ __global__ __launch_bounds__(256) void k_loss_part(const float* __restrict__ z, 
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         const float* row = z + (long long)t * ld;
         MaxSum a{-__builtin_inff(), 0.0f};
-        for (int c = threadIdx.x; c < n; c += 256) a = merge(a, {row[c], row[c] == -__builtin_inff() ? 0.0f : 1.0f});
+#pragma unroll 4
+        for (int c = threadIdx.x; c < n; c += 256) a.m = fmaxf(a.m, row[c]);
+        const float from = a.m == -__builtin_inff() ? 0.0f : a.m;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < n; c += 256) a.s += __builtin_amdgcn_exp2f((row[c] - from) * kLog2e);
         a = merge_lanes<32>(a);
         a = merge_lanes<16>(a);
         a = merge_lanes<8>(a);
@@ -215,22 +292,6 @@ __global__ __launch_bounds__(256) void k_loss_part(const float* __restrict__ z, 
             if (target[t] >= 0 && target[t] < V && at >= 0 && at < n) zt[t] = row[at];
         }
         __syncthreads();
-    }
-}
-
-// d of a piece from its logits (in their place, or as 16-bit rows)
-template <class T>
-__global__ __launch_bounds__(256) void k_loss_d(const float* z, const int64_t* __restrict__ target, const float* __restrict__ lse,
-                                                const float* __restrict__ g, int rows, int V, int v0, int n, int ld,
-                                                T* d) {
-    for (long long t = blockIdx.y; t < rows; t += gridDim.y) {
-        const float gt = g[t], l = lse[t];
-        const int64_t at = target[t] - v0;
-        for (int c = blockIdx.x * 256 + threadIdx.x; c < n; c += gridDim.x * 256) {
-            const float p = __builtin_amdgcn_exp2f((z[t * ld + c] - l) * kLog2e);
-            // an ignored row has no gradient, whatever its logits are
-            d[t * ld + c] = from_f<T>(gt == 0.0f ? 0.0f : (p - (at == c ? 1.0f : 0.0f)) * gt);
-        }
     }
 }
 
@@ -395,31 +456,37 @@ void launch_loss_dx(int dtype, const float* part, int shares, long long n, const
 // ---- the passes --------------------------------------------------------------------
 
 void launch_loss_any(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st) {
+    float2* pairs = (float2*)(scratch + p.pairs);
+    float* zt = (float*)(scratch + p.zt);
+    if (g.T < 1) return;
+    if (!p.logits) {
+        AnyProduct q = any_piece(dtype, g, 0, g.V, nullptr, 0);
+        q.pairs = pairs;
+        q.zt = zt;
+        launch_any_product<kPairs>(dtype, q, st);
+        return;
+    }
     float* logits = (float*)(scratch + p.logits);
-    for (int i = 0; i < p.parts && g.T > 0; ++i) {
+    for (int i = 0; i < p.parts; ++i) {
         const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
-        any_logits(dtype, g, v0, n, p.width, logits, st);
+        launch_any_product<kLogits>(dtype, any_piece(dtype, g, v0, n, logits, p.width), st);
         hipLaunchKernelGGL(k_loss_part, dim3(grid_of(g.T)), dim3(256), 0, st, logits, g.target, g.T, g.V, v0, n, p.width,
-                           (float2*)(scratch + p.pairs) + (long long)i * g.T, (float*)(scratch + p.zt));
+                           pairs + (long long)i * g.T, zt);
     }
 }
 
 void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, const float* lse, char* scratch, void* dx,
                          void* dw, void* db, hipStream_t st) {
     const size_t es = dtype_size(dtype);
-    float *rows = (float*)(scratch + p.g), *logits = (float*)(scratch + p.logits);
+    float* rows = (float*)(scratch + p.g);
     const float* unscale = rows + g.T;
     const bool part = p.pieces * p.shares > 1;
     for (int i = 0; i < p.pieces; ++i) {
         const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
-        any_logits(dtype, g, v0, n, p.width, logits, st);
-        const dim3 grid((unsigned)std::min(ceil_div(n, 256), 64ll), (unsigned)std::min(g.T, 65535));
-        with_dtype(dtype, [&](auto tv) {
-            using T = decltype(tv);
-            if (g.T < 1) return;
-            hipLaunchKernelGGL(k_loss_d<T>, grid, dim3(256), 0, st, logits, g.target, lse, rows, g.T, g.V, v0, n, p.width,
-                               (T*)(scratch + p.d));
-        });
+        AnyProduct z = any_piece(dtype, g, v0, n, scratch + p.d, p.ld);
+        z.lse = lse;
+        z.g = rows;
+        launch_any_product<kD>(dtype, z, st);
         if (db) launch_loss_db(dtype, scratch + p.d, p.ld, g.T, n, unscale, (char*)db + (size_t)v0 * es, st);
         AnyProduct q{};
         q.a = scratch + p.d;
@@ -431,15 +498,15 @@ void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, con
             q.c = part ? scratch + p.dx : dx;
             q.shares = p.shares;
             q.add = i > 0;
-            if (part) launch_any_product<kFormDx, true>(dtype, q, st);
-            else launch_any_product<kFormDx, false>(dtype, q, st);
+            if (part) launch_any_product<kPartDx>(dtype, q, st);
+            else launch_any_product<kDx>(dtype, q, st);
         }
         if (dw) {
             q.b = g.x;
             q.M = n, q.N = g.D, q.K = g.T, q.ldb = g.D, q.ldc = g.D;
             q.c = (char*)dw + (size_t)v0 * g.D * es;
             q.shares = 1;
-            launch_any_product<kFormDw, false>(dtype, q, st);
+            launch_any_product<kDw>(dtype, q, st);
         }
     }
     if (dx && part) launch_loss_dx(dtype, (const float*)(scratch + p.dx), p.shares, (long long)g.T * g.D, unscale, dx, st);

@@ -13,7 +13,12 @@
 namespace lapsum {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr long long kPieceBytes = 256ll << 20;  // of d
+// d of a piece: what the memory-side cache holds, and more, up to four times as
+// much, where dW of so few columns would not fill the CUs with its widest tiles
+// (us with 128 MiB / 256 MiB / 512 MiB / 1 GiB: 8192 rows, 65536 of 2048 5630 /
+// 5430 / 5430 / 5470; 16384, 128256 of 4096 44400 / 42200 / 41200 / 41500; 32768,
+// 32768 of 1024 11200 / 7900 / 7000 / 6030)
+constexpr long long kPieceBytes = 256ll << 20, kMostBytes = 1ll << 30, kPieceWeights = 1 << 24;
 
 static size_t take(size_t& at, size_t bytes) {
     const size_t here = at;
@@ -56,9 +61,10 @@ LS_DEV TileAt tile_at(int rows, int cols, bool cut) {
 
 // ---- forward ---------------------------------------------------------------------
 
-// Up to kFewRows rows a tile's own loads would leave most of it empty; few_tile
-// streams the weights instead (NNN).
-constexpr int kFewRows = 64, kFewCols = 64, kFewWaves = 4;
+// Up to kFewRows rows a tile would be mostly empty, and k_loss_few streams the
+// weights instead (tiles / few, forward over 32768 of 2048 in bf16: 8 rows 43 / 35
+// us, 32 rows 44 / 40, 64 rows 44 / 51).
+constexpr int kFewRows = 32, kFewCols = 64, kFewWaves = 4;
 
 LossParts loss_tile_parts(const LossArgs& g) {
     LossParts p{};
@@ -86,14 +92,13 @@ LS_DEV float across16(float v, bool max_) {  // over the four lanes that share a
     return max_ ? fmaxf(v, o) : v + o;
 }
 
-template <class T, int B>
-__global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int rows, int cols, float2* __restrict__ pairs,
-                                                               float* __restrict__ zt) {
+// A tile of B x B from row i0 and column j0: pairs of `part` and, of the tile's
+// right half, part + 1; MERGE: one pair for both halves.
+template <class T, int B, bool MERGE>
+LS_DEV void loss_tile(const LossArgs& g, int i0, int j0, int part, char* lds, float2* __restrict__ pairs,
+                      float* __restrict__ zt) {
     using Tile = TileSums<T, true, true, B, B>;
-    __shared__ __align__(1024) char lds[Tile::kLds];
-    const TileAt at = tile_at(rows, cols, false);
-    if (at.i < 0) return;
-    const int i0 = at.i * B, j0 = at.j * B, M = g.T - i0, N = g.V - j0;
+    const int M = g.T - i0, N = g.V - j0;
     Tile tile;
     tile.run((const T*)g.x + (long long)i0 * g.D, M, g.D, (const T*)g.w + (long long)j0 * g.D, N, g.D, g.D, lds);
     const int l = lane_id(), w = uniform(threadIdx.x >> 6);
@@ -139,9 +144,21 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int r
 #pragma unroll
             for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(fmaf(v[j][r], kLog2e, from));
         s = across16(s, false);
+        if (MERGE) {
+            float2* half = (float2*)lds + row;  // (the sums' buffers are free)
+            if (w & 1) *half = make_float2(m, s);
+            __syncthreads();
+            if (!(w & 1)) {
+                const float2 o = *half;
+                const float top = fmaxf(m, o.x), at = top == -__builtin_inff() ? 0.0f : top;
+                s = s * __builtin_amdgcn_exp2f((m - at) * kLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - at) * kLog2e);
+                m = top;
+                if (l < 16 && row < M) pairs[(long long)part * g.T + i0 + row] = make_float2(m, s);
+            }
+        } else if (l < 16 && row < M) {
+            pairs[(long long)(part + (w & 1)) * g.T + i0 + row] = make_float2(m, s);
+        }
         if (row >= M) continue;
-        const int part = at.j * 2 + (w & 1);
-        if (l < 16) pairs[(long long)part * g.T + i0 + row] = make_float2(m, s);
         // the target, if this lane holds it
         const int64_t c = target[i] - j0 - c0;
         if (target[i] < 0 || target[i] >= g.V || c < 0 || c >= B / 2 || (c & 31) >> 3 != l >> 4) continue;
@@ -155,13 +172,37 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int r
     }
 }
 
-// 16 FM rows and kFewCols columns: bound by reading the weights, once.  The
+template <class T, int B>
+__global__ __launch_bounds__(kProductThreads) void k_loss_tile(LossArgs g, int rows, int cols, float2* __restrict__ pairs,
+                                                               float* __restrict__ zt) {
+    __shared__ __align__(1024) char lds[TileSums<T, true, true, B, B>::kLds];
+    const TileAt at = tile_at(rows, cols, B == 256);
+    if (at.i < 0) return;
+    if constexpr (B == 256) {
+        if (at.quarter >= 0) {
+            const int i0 = at.i * B + (at.quarter >> 1) * (B / 2), j0 = at.j * B + (at.quarter & 1) * (B / 2);
+            const int part = at.j * 2 + (at.quarter & 1);
+            if (i0 < g.T && j0 < g.V) {
+                loss_tile<T, B / 2, true>(g, i0, j0, part, lds, pairs, zt);
+            } else if (threadIdx.x < B / 2 && i0 + (int)threadIdx.x < g.T) {  // no columns
+                pairs[(long long)part * g.T + i0 + threadIdx.x] = make_float2(-__builtin_inff(), 0.0f);
+            }
+            return;
+        }
+    }
+    loss_tile<T, B, false>(g, at.i * B, at.j * B, at.j * 2, lds, pairs, zt);
+}
+
+// 16 FM rows and kFewCols columns of the piece v0 .. v0 + n - 1, to pairs or (GRAD)
+// to d, as k_loss_dtile: bound by reading the weights, once.  The
 // waves split the sum; each multiplies its share straight from memory (a weight
 // is used once, so LDS would only add a stop on its way), and their sums meet in
 // LDS, added in wave order.
-template <class T, int FM>
-__global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, float2* __restrict__ pairs,
-                                                              float* __restrict__ zt) {
+template <class T, int FM, bool GRAD>
+__global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, int v0, int n, float2* __restrict__ pairs,
+                                                              float* __restrict__ zt, int ld,
+                                                              const float* __restrict__ lse,
+                                                              const float* __restrict__ grad, T* __restrict__ d) {
     constexpr int FN = kFewCols / 16, U = FM == 1 ? 4 : 2;  // steps of 32 k in flight
     constexpr int kPad = kFewCols + 4;
     __shared__ float part[kFewWaves][16][kPad];
@@ -173,7 +214,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, float2*
 #pragma unroll
     for (int i = 0; i < FM; ++i) x[i] = (const T*)g.x + (long long)min(i * 16 + i16, g.T - 1) * D + k8;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) b[j] = (const T*)g.w + (long long)min(j0 + j * 16 + i16, g.V - 1) * D + k8;
+    for (int j = 0; j < FN; ++j) b[j] = (const T*)g.w + (long long)(v0 + min(j0 + j * 16 + i16, n - 1)) * D + k8;
     f32x4 acc[FM][FN] = {};
     const int steps = (D + 31) / 32, whole = D / 32, s1 = (w + 1) * steps / kFewWaves;
     int s = w * steps / kFewWaves;
@@ -210,7 +251,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, float2*
     float add[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        add[r] = j0 + c + r >= g.V ? -__builtin_inff() : g.bias ? to_f(((const T*)g.bias)[j0 + c + r]) : 0.0f;
+        add[r] = j0 + c + r >= n ? -__builtin_inff() : g.bias ? to_f(((const T*)g.bias)[v0 + j0 + c + r]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         if (i) __syncthreads();
@@ -222,6 +263,19 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, float2*
         f32x4 v = *(const f32x4*)&part[0][row][c];
 #pragma unroll
         for (int p = 1; p < kFewWaves; ++p) v += *(const f32x4*)&part[p][row][c];
+        const int64_t at = g.target[t] - v0 - j0 - c;
+        if constexpr (GRAD) {
+            const float gt = grad[t], lo = lse[t] * -kLog2e;
+            struct __attribute__((aligned(8))) T4 { T v[4]; } o;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(v[r] + add[r], kLog2e, lo));
+                const bool on = gt != 0.0f && j0 + c + r < n;
+                o.v[r] = from_f<T>(on ? (p - (at == r ? 1.0f : 0.0f)) * gt : 0.0f);
+            }
+            if (j0 + c < ld) *(T4*)(d + (long long)t * ld + j0 + c) = o;  // ld is a multiple of 8
+            continue;
+        }
         float m = -__builtin_inff();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -241,27 +295,31 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, float2*
         sum += __uint_as_float(xor_lane<2>(__float_as_uint(sum)));
         sum += __uint_as_float(xor_lane<1>(__float_as_uint(sum)));
         if (c == 0) pairs[(long long)blockIdx.x * g.T + t] = make_float2(m, sum);
-        const int64_t target = g.target[t], at = target - j0 - c;
-        if (target < 0 || target >= g.V || at < 0 || at >= 4) continue;
+        if (at < 0 || at >= 4 || g.target[t] >= g.V) continue;
         zt[t] = at == 0 ? v[0] : at == 1 ? v[1] : at == 2 ? v[2] : v[3];
     }
 }
 
+template <bool GRAD>
+static void launch_few(int dtype, const LossArgs& g, int v0, int n, float2* pairs, float* zt, int ld, const float* lse,
+                       const float* grad, void* d, hipStream_t st) {
+    with_dtype(dtype, [&](auto tv) {
+        using T = decltype(tv);
+        if constexpr (sizeof(T) == 2) {
+            auto launch = [&](auto fm) {
+                hipLaunchKernelGGL((k_loss_few<T, fm.value, GRAD>), dim3((unsigned)ceil_div(n, kFewCols)),
+                                   dim3(kFewWaves * 64), 0, st, g, v0, n, pairs, zt, ld, lse, grad, (T*)d);
+            };
+            if (g.T <= 16) launch(std::integral_constant<int, 1>{});
+            else launch(std::integral_constant<int, 2>{});
+        }
+    });
+}
+
 void launch_loss_tile(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st) {
     if (g.T <= kFewRows) {
-        with_dtype(dtype, [&](auto tv) {
-            using T = decltype(tv);
-            if constexpr (sizeof(T) == 2) {
-                auto launch = [&](auto fm) {
-                    hipLaunchKernelGGL((k_loss_few<T, fm.value>), dim3((unsigned)ceil_div(g.V, kFewCols)),
-                                       dim3(kFewWaves * 64), 0, st, g, (float2*)(scratch + p.pairs),
-                                       (float*)(scratch + p.zt));
-                };
-                if (g.T <= 16) launch(std::integral_constant<int, 1>{});
-                else if (g.T <= 32) launch(std::integral_constant<int, 2>{});
-                else launch(std::integral_constant<int, 4>{});
-            }
-        });
+        launch_few<false>(dtype, g, 0, g.V, (float2*)(scratch + p.pairs), (float*)(scratch + p.zt), 0, nullptr, nullptr,
+                          nullptr, st);
         return;
     }
     with_side(side_of(g.T, g.V), [&](auto bv) {
@@ -270,7 +328,7 @@ void launch_loss_tile(int dtype, const LossArgs& g, const LossParts& p, char* sc
         with_dtype(dtype, [&](auto tv) {
             using T = decltype(tv);
             if constexpr (sizeof(T) == 2)
-                hipLaunchKernelGGL((k_loss_tile<T, B>), dim3((unsigned)turns(rows * cols, false)), dim3(kProductThreads), 0,
+                hipLaunchKernelGGL((k_loss_tile<T, B>), dim3((unsigned)turns(rows * cols, B == 256)), dim3(kProductThreads), 0,
                                    st, g, (int)rows, (int)cols, (float2*)(scratch + p.pairs), (float*)(scratch + p.zt));
         });
     });
@@ -280,7 +338,9 @@ void launch_loss_tile(int dtype, const LossArgs& g, const LossParts& p, char* sc
 
 LossVjpPlan loss_tile_plan(const LossArgs& g) {
     LossVjpPlan p{};
-    const long long most = std::max(kPieceBytes / 2 / std::max(g.T, 1) / 256 * 256, 256ll);
+    const auto columns = [&](long long bytes) { return bytes / 2 / g.T / 256 * 256; };
+    const long long fill = ceil_div(kPieceWeights, 256ll * g.D) * 256;
+    const long long most = std::max({columns(kPieceBytes), std::min(fill, columns(kMostBytes)), 256ll});
     p.width = (int)std::min<long long>(std::min(most, 1ll << 18), g.V);
     p.ld = (p.width + 7) & ~7;
     p.pieces = (int)ceil_div(g.V, p.width);
@@ -433,7 +493,8 @@ void launch_loss_tile_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, co
     const bool part = p.pieces * p.shares > 1;
     for (int i = 0; i < p.pieces; ++i) {
         const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
-        with_side(side_of(g.T, n), [&](auto bv) {
+        if (g.T <= kFewRows) launch_few<true>(dtype, g, v0, n, nullptr, nullptr, p.ld, lse, rows, scratch + p.d, st);
+        else with_side(side_of(g.T, n), [&](auto bv) {
             constexpr int B = bv.value;
             const long long r = ceil_div(g.T, B), c = ceil_div(n, B);
             with_dtype(dtype, [&](auto tv) {

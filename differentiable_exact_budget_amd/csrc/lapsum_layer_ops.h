@@ -29,24 +29,24 @@ enum Reduction : int { kReduceNone = 0, kReduceSum = 1, kReduceMean = 2 };
 
 // The gradient's pieces of the vocabulary, and its scratch (all offsets in
 // bytes, each on 256): g[T] and the inverse of its scale, d[T, ld] of one
-// piece, logits[T, width] of one piece (where they are formed by themselves),
-// dx's partial sums [shares, T, D] (where there is more than one).
+// piece, dx's partial sums [shares, T, D] (where there is more than one).
 struct LossVjpPlan {
     int width;   // columns of a piece
     int ld;      // elements between rows of d: the width on a multiple of 8
     int pieces;
     int shares;  // of dx's sum over a piece
-    size_t g, d, logits, dx, bytes;
+    size_t g, d, dx, bytes;
 };
 
 // lapsum_entropy.hip: every type, width and alignment, and the steps around the
 // products
 struct LossParts {
     int parts;           // partial (maximum, sum) pairs of a row
-    size_t pairs, zt, loss, logits, bytes;  // scratch, as above; pairs[parts][T]
-    int width;           // columns of a piece of logits
+    size_t pairs, zt, loss, bytes;  // scratch, as above; pairs[parts][T]
+    size_t logits;       // [T, width] of one piece, where they are formed by themselves (else 0)
+    int width;
 };
-LossParts loss_any_parts(const LossArgs& g);
+LossParts loss_any_parts(int dtype, const LossArgs& g);
 LossVjpPlan loss_any_plan(int dtype, const LossArgs& g);
 void launch_loss_any(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st);
 void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, const float* lse, char* scratch, void* dx,

@@ -67,7 +67,7 @@ size_t lapsum_linear_cross_entropy_scratch_bytes(lapsum_dtype_t dtype, int64_t r
     if (!good_loss(dtype, rows, vocab, width)) return 0;
     const LossArgs g = loss_args(nullptr, nullptr, nullptr, nullptr, rows, vocab, width);
     // whatever the addresses' alignment
-    const size_t any = loss_any_parts(g).bytes;
+    const size_t any = loss_any_parts(dtype, g).bytes;
     return loss_tile_takes(dtype, g) ? std::max(any, loss_tile_parts(g).bytes) : any;
 }
 
@@ -86,7 +86,7 @@ lapsum_status_t lapsum_linear_cross_entropy(const void* x, const void* weight, c
     float* each = loss;
     if (rows > 0) {
         const bool tile = loss_tile_takes(dtype, g);
-        const LossParts p = tile ? loss_tile_parts(g) : loss_any_parts(g);
+        const LossParts p = tile ? loss_tile_parts(g) : loss_any_parts(dtype, g);
         if (tile) launch_loss_tile(dtype, g, p, s, st);
         else launch_loss_any(dtype, g, p, s, st);
         if (reduction != LAPSUM_REDUCE_NONE) each = reinterpret_cast<float*>(s + p.loss);

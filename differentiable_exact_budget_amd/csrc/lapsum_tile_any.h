@@ -77,11 +77,19 @@ struct AnyOperand : StepLds<R, KFAST, PAIRED> {
     }
 };
 
+// whether an output takes the sums of a shared tile with cell() (below)
+template <class P, class = void>
+struct HasCell : std::false_type {};
+template <class P>
+struct HasCell<P, std::void_t<decltype(&P::cell)>> : std::true_type {};
+
 // The sums over k < K of a(i, k) b(j, k) of a B x B tile; SPLIT: the waves share
 // the sum.  a, b: element (0, 0) of the tile; kA, kB: k is the contiguous index;
 // M, N: rows and columns that there are from there (1 and more); lda, ldb:
 // elements between memory rows.  put.one(i, j, v) takes a sum of the M x N,
-// put.eight(i, j, v) eight of a row, whose columns may pass N.
+// put.eight(i, j, v) eight of a row, whose columns may pass N.  With SPLIT,
+// put.cell(i, j, v, on), if there is one, takes every place of the tile, B
+// neighbouring lanes a row of it, `on` where it is one of the M x N.
 template <class T, bool kA, bool kB, int B, bool SPLIT, class Put>
 LS_DEV void any_sums(const T* a, int M, int lda, const T* b, int N, int ldb, int K_, char* lds, const Put& put) {
     constexpr bool k16 = sizeof(T) == 2;
@@ -213,7 +221,8 @@ LS_DEV void any_sums(const T* a, int M, int lda, const T* b, int N, int ldb, int
             float v = part[i * kPad + j];
 #pragma unroll
             for (int o = 1; o < 4; ++o) v += part[(o * B + i) * kPad + j];
-            if (i < M && j < N) put.one(i, j, v);
+            if constexpr (HasCell<Put>::value) put.cell(i, j, v, i < M && j < N);
+            else if (i < M && j < N) put.one(i, j, v);
         }
     } else {
         each([&](int i, int j, float v) {
