@@ -387,10 +387,8 @@ __global__ __launch_bounds__(1024) void k_loss_grad_rows(const float* __restrict
     for (int i = 0; i < 16; ++i) count += c[i];
     const float div = reduction == kReduceMean ? (float)max(count, 1u) : 1.0f;
     int e = 0;
-    if (SCALED && top) {
-        e = 13 - (ilogbf(__uint_as_float(top) / div));
-        e = min(max(e, -100), 100);
-    }
+    const float most = __uint_as_float(top) / div;
+    if (SCALED && most > 0.0f) e = min(max(13 - ilogbf(most), -100), 100);
     const float scale = ldexpf(1.0f, e);
     for (int t = threadIdx.x; t < T; t += 1024) {
         const bool on = target[t] >= 0 && target[t] < V;

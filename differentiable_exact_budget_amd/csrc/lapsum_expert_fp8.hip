@@ -23,7 +23,8 @@
 // fp32), which leaves sums of random rows 1.5e-5 off in the 2-norm, whatever
 // their length: a thirtieth of fp16's rounding.  Results in fp32 take the bf16
 // instruction instead, on values expanded in registers, scales and all: e4m3
-// fits bf16, so the products are exact and the sums fp32's own.
+// fits bf16 down to 2^-126 (below, a value keeps bf16's nearest multiple of
+// 2^-133), so the products are exact and the sums fp32's own.
 #include "lapsum_layer_ops.h"
 #include "lapsum_tile_mfma.h"
 

@@ -266,6 +266,8 @@ void check_rows8(const Tensor& values, const Tensor& scales, int64_t width, cons
                       at::IntArrayRef(shape), " (got ", scales.sizes(), ")");
     TORCH_CHECK_VALUE(values.is_contiguous() && scales.is_contiguous(), name, " must be contiguous");
     TORCH_CHECK_VALUE((reinterpret_cast<uintptr_t>(values.data_ptr()) & 15) == 0, name, ".values must start on 16 bytes");
+    TORCH_CHECK(!(at::GradMode::is_enabled() && (recorded(values) || recorded(scales))), name,
+                " in 8 bits have no gradient: detach them");
 }
 
 std::tuple<Tensor, Tensor> quantize(const Tensor& x_) {

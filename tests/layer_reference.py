@@ -150,7 +150,10 @@ def linear8(xs, weight, bias, offsets, a, dtype):
 
     For 16-bit results the matrix instruction drops from each product of eight
     neighbours what is below 2^-13 of the largest one's power of two: seven times
-    that is lost at most."""
+    that is lost at most.  For float32 results the operands are in bf16, which
+    holds e4m3's four bits down to its least step, 2^-133, of which a smaller
+    number keeps the nearest multiple: each operand is off by 2^-134 at most, which
+    counts by the other one's magnitude."""
     groups = lambda v: torch.nn.functional.pad(v.abs(), (0, -v.shape[-1] % 8)).unflatten(-1, (-1, 8)).amax(-1)  # noqa: E731
     P, K = xs.shape
     E, F, _ = weight.shape
@@ -165,7 +168,10 @@ def linear8(xs, weight, bias, offsets, a, dtype):
             z = z + bias[e].double()
             mag = mag + bias[e].double().abs()
         y[r] = act(z, a)
-        lost = 7 * 2.0 ** -13 * (groups(xs[r]) @ groups(weight[e]).t()) if dtype != torch.float32 and K else 0
+        if dtype != torch.float32:
+            lost = 7 * 2.0 ** -13 * (groups(xs[r]) @ groups(weight[e]).t()) if K else 0
+        else:
+            lost = 2.0 ** -134 * (xs[r].abs().sum(1, keepdim=True) + weight[e].abs().sum(1))
         err[r] = 1.13 * ((K + 2) * EPS * mag + lost) + (0 if a == "none" else 16 * EPS * z.abs())
         if a == "gelu" and dtype != torch.float32:  # the polynomial tail, 2.1e-4 Q(|z|) off at most
             err[r] += 2.2e-4 * z.abs() * 0.5 * torch.erfc(z.abs() / math.sqrt(2)) + 4e-7 * z.abs()

@@ -504,6 +504,45 @@ def test_products_in_8_bits_of_values_that_are_not_finite_stay_in_their_row():
     assert torch.equal(got[rest], want[rest]) and got[[5, 17]].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_products_in_8_bits_of_the_least_and_of_missing_scales(dtype):
+    """Scales from 2^-127 on, whose products come back into range, and scales of
+    NaN, which make their row (of the rows) or column (of the weights) NaN."""
+    g = gen(8)
+    K, F, P = 256, 40, 70
+    xs = torch.randn(P, K, generator=g) * torch.exp2(torch.randint(-126, -100, (P, 1), generator=g).float())
+    xs[:8] = torch.randn(8, K, generator=g) * 2.0 ** -128
+    w = torch.randn(1, F, K, generator=g) * 2.0 ** 110
+    plan = L.expert_sort(torch.zeros(P, 1, dtype=torch.int32, device="cuda"), 1)
+    o = torch.tensor([0, P])
+    want = check_product8(plan, o, xs, w, None, "none", dtype)
+    assert want.abs().max() > 0
+    qx, qw = L.expert_quantize(xs.cuda()), L.expert_quantize(w.cuda())
+    assert int(qx.scales.view(torch.uint8).min()) == 0
+    qx.scales.view(torch.uint8)[5, 1] = 255
+    qw.scales.view(torch.uint8)[0, 33, 0] = 255
+    got = L.expert_linear_fp8(qx, qw, plan, dtype=dtype)
+    bad = torch.zeros(P, F, dtype=torch.bool)
+    bad[5], bad[:, 33] = True, True
+    assert torch.equal(got.isnan().cpu(), bad) and torch.equal(got.cpu()[~bad], want.cpu()[~bad])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_products_in_8_bits_by_a_plan_from_elsewhere_stay_in_bounds(dtype):
+    """Offsets that run back or past the rows: rows may be wrong, and nothing
+    outside the arrays is read or written (the results have guards around them)."""
+    P, E, K, F = 600, 6, 256, 136
+    g = gen(12)
+    qx = L.expert_quantize(torch.randn(P, K, generator=g).cuda())
+    qw = L.expert_quantize(torch.randn(E, F, K, generator=g).cuda())
+    for off in ([0, P] * 3 + [0], [0, 900, 100, -5, 2 ** 31 - 1, 700, 650], [P] * 7, [-(2 ** 31)] * 7):
+        plan = L.ExpertPlan(E, torch.tensor(off, dtype=torch.int32).cuda(), torch.zeros(P, dtype=torch.int32).cuda(),
+                            torch.zeros(P // 2, 2, dtype=torch.int32).cuda())
+        y = L.expert_linear_fp8(qx, qw, plan, dtype=dtype)
+        assert y.shape == (P, F)
+    torch.cuda.synchronize()
+
+
 # ---- refusals --------------------------------------------------------------------
 
 def test_refusals():
@@ -549,7 +588,9 @@ def test_refusals():
         with pytest.raises(TypeError):
             f()
     bias = torch.zeros(2, 16, device=dev, dtype=torch.bfloat16, requires_grad=True)
-    for f in (lambda: L.expert_quantize(x.detach().requires_grad_(True)), lambda: L.expert_linear_fp8(q, qw, plan, bias=bias)):
+    kept = L.ScaledRows(q.values.detach().requires_grad_(True), q.scales, 128)
+    for f in (lambda: L.expert_quantize(x.detach().requires_grad_(True)), lambda: L.expert_linear_fp8(q, qw, plan, bias=bias),
+              lambda: L.expert_dequantize(kept), lambda: L.expert_linear_fp8(kept, qw, plan)):
         with pytest.raises(RuntimeError, match="no gradient"):
             f()
         with torch.no_grad():
@@ -679,7 +720,7 @@ def test_a_model_of_them(dtype):
     want = torch.nn.functional.cross_entropy(z, target)
     wants = torch.autograd.grad(want * scale, [xr] + [ref[k] for k in names])
     u = R.U[dtype] / math.sqrt(3)
-    assert abs(float(loss.detach()) - float(want)) < 12 * u * abs(float(want)) + 1e-5
+    assert abs(float(loss.detach()) - float(want.detach())) < 12 * u * abs(float(want.detach())) + 1e-5
     for name, got, w in zip(["x"] + names, grads, wants):
         rel = float((got.double() - w).norm() / w.norm())
         assert rel < 12 * u + 2e-5, (name, rel)
@@ -745,3 +786,62 @@ def test_graph_replays_follow_new_inputs(T, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, step())), i
+
+
+# ---- offsets beyond 32 bits ---------------------------------------------------------
+
+@pytest.mark.slow
+def test_norm_and_8_bits_past_2_to_the_31_elements():
+    T, D = 270_000, 8192  # 2.2e9 elements
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    for r in range(0, T, 30_000):
+        x[r:r + 30_000].normal_()
+    w = torch.rand(D, device="cuda") + 0.5
+    y, mean, rstd = L.layer_norm_forward(x, w)
+    at = torch.tensor([0, 1, T // 2, T - 70_000, T - 2, T - 1], device="cuda")
+    few, _, _ = L.layer_norm_forward(x[at], w)
+    assert torch.equal(y[at], few)
+    dx, _, _ = L.layer_norm_vjp(x, w, mean, rstd, y, want=(True, False, False))
+    want, _, _ = L.layer_norm_vjp(x[at], w, mean[at], rstd[at], y[at], want=(True, False, False))
+    assert torch.equal(dx[at], want)
+    del dx, y
+    rows, part = L.expert_quantize(x), L.expert_quantize(x[at])
+    assert torch.equal(rows.values.view(torch.uint8)[at], part.values.view(torch.uint8))
+    assert torch.equal(L.expert_dequantize(rows)[at], L.expert_dequantize(part))
+    # as rows of a product, and as its weights
+    plan = L.expert_sort(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1)
+    qw = L.expert_quantize(torch.randn(1, 16, D, device="cuda"))
+    ys = L.expert_linear_fp8(rows, qw, plan)
+    one = L.expert_sort(torch.zeros(6, 1, dtype=torch.int32, device="cuda"), 1)
+    assert torch.equal(ys[at], L.expert_linear_fp8(part, qw, one))
+    wide = L.ScaledRows(rows.values.reshape(2, T // 2, D), rows.scales.reshape(2, T // 2, D // 128), D)
+    two = L.expert_sort(torch.tensor([[0], [1], [1]], dtype=torch.int32, device="cuda"), 2)
+    q3 = L.expert_quantize(torch.randn(3, D, device="cuda"))
+    ys = L.expert_linear_fp8(q3, wide, two)
+    v = L.ScaledRows(part.values[3:].reshape(1, 3, D), part.scales[3:].reshape(1, 3, D // 128), D)
+    three = L.expert_sort(torch.zeros(3, 1, dtype=torch.int32, device="cuda"), 1)
+    assert torch.equal(ys[1:, at[3:] - T // 2], L.expert_linear_fp8(q3, v, three)[1:])
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("T", [8, 200])
+def test_loss_of_a_vocabulary_past_2_to_the_31_elements(T):
+    """The far end of the weights against the same rows taken alone: entries
+    without a share of the sums are masked."""
+    V, D = 270_000, 8192
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    for r in range(0, V, 30_000):
+        w[r:r + 30_000].normal_().mul_(D ** -0.5)
+    x = torch.randn(T, D, device="cuda").bfloat16()
+    n = 1000
+    bias = torch.full((V,), -math.inf, dtype=torch.bfloat16, device="cuda")
+    bias[-n:] = 0
+    target = torch.randint(V - n, V, (T,), device="cuda")
+    loss, lse = L.linear_cross_entropy_forward(x, w, target, bias=bias, reduction="none")
+    few, few_lse = L.linear_cross_entropy_forward(x, w[-n:], target - (V - n), reduction="none")
+    ref = R.loss(x, w[-n:], None, target - (V - n), "none", torch.ones(T, device="cuda"))
+    X.check(loss, *ref["loss"], "loss")
+    dx, dw, _ = L.linear_cross_entropy_vjp(x, w, target, lse, torch.ones(T, device="cuda"), bias=bias, reduction="none")
+    X.check(dx, *ref["dx"], "dx")
+    X.check(dw[-n:], *ref["dw"], "dw")
+    assert dw[:-n:1001].abs().max() == 0 and dw[V - n - 1].abs().max() == 0
