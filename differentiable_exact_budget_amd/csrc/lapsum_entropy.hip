@@ -13,9 +13,9 @@
 // Here the products are those for any alignment (lapsum_tile_any.h).  Tiles of
 // 32 columns reduce them as they are; wide tiles' logits go through scratch in
 // fp32, a piece of the vocabulary at a time.  d is rounded to the rows'
-// type once, because the matrix instructions take it so; for fp16, whose range
-// ends at 6e-8, d is scaled by a power of two that brings the largest gradient
-// of a row's loss to 2^13 .. 2^14, and the products are scaled back in fp32.
+// type once, because the matrix instructions take it so; its rows are taken over
+// the largest gradient of a row's loss (k_loss_grad_rows), and the products are
+// multiplied by that again in fp32.
 #include "lapsum_layer_ops.h"
 #include "lapsum_tile_any.h"
 
@@ -31,10 +31,18 @@ static size_t take(size_t& at, size_t bytes) {
     return here;
 }
 
-// As for the experts' products: 128 x 128 tiles where there are enough and rows to
-// fill them, else 32 x 32 with the sum shared by the waves.
-static bool wide_tiles(int dtype, long long M, long long N, int shares) {
-    return std::min(M, N) > 64 && ceil_div(N, 128) * ceil_div(M, 128) * shares >= (dtype == kF32 ? 384 : 128);
+// The side of a product's tiles, which 32-wide ones share among a workgroup's
+// waves: for 16-bit rows as for the experts' products; for fp32, whose wide tiles
+// take long, 128 from three rounds of them on, and 64 before (forward, us, 128 /
+// 64 / 32: 4096 rows over 8192 of 1024 576 / 620 / -; 2000 over 3000 of 512 85 / 79
+// / -; 156 over 43301 of 3624 984 / 594 / -; 300 over 5000 of 333 44 / 30 / 35; 513
+// over 1001 of 257 37 / 21 / 17).
+static int any_side(int dtype, long long M, long long N, int shares) {
+    const auto tiles = [&](int side) { return ceil_div(M, side) * ceil_div(N, side) * shares; };
+    const long long least = std::min(M, N);
+    if (dtype != kF32) return least > 64 && tiles(128) >= 128 ? 128 : 32;
+    if (least > 64 && tiles(128) >= 1536) return 128;
+    return least > 32 && tiles(64) >= 320 ? 64 : 32;
 }
 
 static int any_width(const LossArgs& g) {
@@ -46,7 +54,7 @@ LossParts loss_any_parts(int dtype, const LossArgs& g) {
     LossParts p{};
     p.width = any_width(g);
     // narrow tiles reduce their columns themselves
-    const bool logits = wide_tiles(dtype, g.T, std::min(p.width, g.V), 1);
+    const bool logits = any_side(dtype, g.T, std::min(p.width, g.V), 1) > 32;
     p.parts = (int)(logits ? ceil_div(g.V, p.width) : ceil_div(g.V, 32));
     size_t at = 0;
     p.pairs = take(at, (size_t)p.parts * g.T * sizeof(float2));
@@ -57,10 +65,17 @@ LossParts loss_any_parts(int dtype, const LossArgs& g) {
     return p;
 }
 
-// dx's sum over a piece is shared out where its tiles are few
-static int any_shares(const LossArgs& g, int width) {
-    const long long tiles = ceil_div(g.T, 32) * ceil_div(g.D, 32);
-    return (int)std::max(1ll, std::min<long long>(512 / std::max(tiles, 1ll), width / 512));
+// The shares of dx's sum over a piece: as many as make enough wide tiles (156 rows
+// of 3624 over 43301 in fp32: 3900 us unshared, 550 in seven), or enough narrow
+// ones where there are few rows.
+static int any_shares(int dtype, const LossArgs& g, int width) {
+    const auto shares = [&](long long need, int side, int least) {
+        const long long tiles = std::max(ceil_div(g.T, side) * ceil_div(g.D, side), 1ll);
+        return (int)std::max(1ll, std::min<long long>(ceil_div(need, tiles), width / least));
+    };
+    const int wide = dtype == kF32 ? shares(1024, 64, 1024) : shares(128, 128, 1024);
+    if (any_side(dtype, g.T, g.D, wide) > 32) return wide;
+    return shares(512, 32, 512);
 }
 
 LossVjpPlan loss_any_plan(int dtype, const LossArgs& g) {
@@ -68,7 +83,7 @@ LossVjpPlan loss_any_plan(int dtype, const LossArgs& g) {
     p.width = any_width(g);
     p.ld = p.width;
     p.pieces = (int)ceil_div(g.V, p.width);
-    p.shares = any_shares(g, p.width);
+    p.shares = any_shares(dtype, g, p.width);
     size_t at = 0;
     p.g = take(at, ((size_t)g.T + 1) * 4);
     p.d = take(at, (size_t)g.T * p.width * dtype_size(dtype));
@@ -223,8 +238,11 @@ static void launch_any_product(int dtype, const AnyProduct& g, hipStream_t st) {
         if constexpr (USE == kPairs) {
             launch(std::integral_constant<int, 32>{}, std::true_type{});
         } else {
-            const bool wide = USE == kLogits || wide_tiles(dtype, g.M, g.N, g.shares);
-            if (wide) launch(std::integral_constant<int, 128>{}, std::false_type{});
+            const int side = any_side(dtype, g.M, g.N, g.shares);
+            constexpr bool k32 = sizeof(T) == 4;
+            if (side == 128) launch(std::integral_constant<int, 128>{}, std::false_type{});
+            // (the last piece of logits may have fewer tiles than the others)
+            else if (side == 64 || USE == kLogits) launch(std::integral_constant<int, k32 ? 64 : 128>{}, std::false_type{});
             else if constexpr (USE != kLogits) launch(std::integral_constant<int, 32>{}, std::true_type{});
         }
     });
@@ -363,9 +381,12 @@ void launch_loss_reduce(const LossArgs& g, const float* loss, int reduction, flo
                        out);
 }
 
-// The gradient of every row's loss, 0 for an ignored row, one workgroup.
-// SCALED (fp16): times the power of two that brings the largest to 2^13 ..
-// 2^14; its inverse stands behind them.
+// The gradient of every row's loss over the largest one's magnitude, 0 for an
+// ignored row; behind them what the products are multiplied by again.  One
+// workgroup.  So d is p - onehot itself where all rows have one gradient, and is
+// rounded row by row (times a common factor, the factor's rounding was in all
+// rows alike: up to 2^-9 of dx and dW in bf16).  SCALED (fp16): times 2^13,
+// which keeps small shares of the softmax above the type's least numbers.
 template <bool SCALED>
 __global__ __launch_bounds__(1024) void k_loss_grad_rows(const float* __restrict__ dloss, const int64_t* __restrict__ target,
                                                          int T, int V, int reduction, float* __restrict__ g) {
@@ -386,15 +407,12 @@ __global__ __launch_bounds__(1024) void k_loss_grad_rows(const float* __restrict
     count = 0;
     for (int i = 0; i < 16; ++i) count += c[i];
     const float div = reduction == kReduceMean ? (float)max(count, 1u) : 1.0f;
-    int e = 0;
-    const float most = __uint_as_float(top) / div;
-    if (SCALED && most > 0.0f) e = min(max(13 - ilogbf(most), -100), 100);
-    const float scale = ldexpf(1.0f, e);
+    const float most = top ? __uint_as_float(top) : 1.0f, scale = SCALED ? 8192.0f : 1.0f;
     for (int t = threadIdx.x; t < T; t += 1024) {
         const bool on = target[t] >= 0 && target[t] < V;
-        g[t] = on ? dloss[reduction == kReduceNone ? t : 0] / div * scale : 0.0f;
+        g[t] = on ? dloss[reduction == kReduceNone ? t : 0] / most * scale : 0.0f;
     }
-    if (threadIdx.x == 0) g[T] = ldexpf(1.0f, -e);
+    if (threadIdx.x == 0) g[T] = most / div / scale;
 }
 void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int reduction, float* rows,
                            hipStream_t st) {

@@ -28,7 +28,7 @@ struct LossArgs {
 enum Reduction : int { kReduceNone = 0, kReduceSum = 1, kReduceMean = 2 };
 
 // The gradient's pieces of the vocabulary, and its scratch (all offsets in
-// bytes, each on 256): g[T] and the inverse of its scale, d[T, ld] of one
+// bytes, each on 256): g[T] and its factor, d[T, ld] of one
 // piece, dx's partial sums [shares, T, D] (where there is more than one).
 struct LossVjpPlan {
     int width;   // columns of a piece
@@ -54,7 +54,7 @@ void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, con
 // lse and, with loss (may be null), the rows' losses; then their sum or mean
 void launch_loss_rows(const LossArgs& g, const LossParts& p, char* scratch, float* loss, float* lse, hipStream_t st);
 void launch_loss_reduce(const LossArgs& g, const float* loss, int reduction, float* out, hipStream_t st);
-// g[t], scaled by a power of two, and its inverse behind it
+// g[t] over the largest, and what results are multiplied by behind it
 void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int reduction, float* rows,
                            hipStream_t st);
 void launch_loss_db(int dtype, const void* d, int ld, int T, int n, const float* unscale, void* db, hipStream_t st);

@@ -98,9 +98,9 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
     logit of +inf or NaN, or with nothing but -inf, has a loss of NaN or inf.
 
     Differentiable with respect to x, weight and bias.  The logits are formed
-    again for the gradient, a piece of the vocabulary at a time, and their
-    gradient is rounded once to the rows' type before the products that follow;
-    16-bit floats with 5 bits of exponent are scaled against underflow there."""
+    again for the gradient, a piece of the vocabulary at a time; their gradient,
+    over the largest of the rows' losses, is rounded once to the rows' type for
+    the products that follow, which hold their sums and the factor in float32."""
     _tensors(x=x, weight=weight, target=target)
     return _native().linear_cross_entropy(x, weight, target, bias, reduction)
 

@@ -72,8 +72,8 @@ lapsum_status_t lapsum_linear_cross_entropy(const void* x, const void* weight, c
                                             void* scratch, lapsum_stream_t stream);
 
 /*
- * With d = (e^(z - lse) - onehot) times the gradient of a row's loss, rounded
- * to dtype once: dx = d W, dweight = d^T x, dbias = the sum of d over the rows.
+ * With d = (e^(z - lse) - onehot) times the gradient of a row's loss, over the
+ * largest such gradient rounded to dtype once: dx = d W, dweight = d^T x, dbias = the sum of d over the rows.
  *   lse   : the forward's.
  *   dloss : fp32, the gradient of what the forward returned: [rows], or [1]
  *           with a reduction.  A row whose gradient is 0 adds nothing, whatever

@@ -59,8 +59,8 @@ def loss(x, weight, bias, target, reduction, dloss=None):
     z is a sum of D products and a bias in fp32.  The sum of exponentials is
     taken in parts, at most 64 + V / 16 deep; an exponential is off by 2 ulp and by
     its argument's rounding, 3 EPS a of a term e^-a, which is at most 1.2 EPS of the
-    sum.  d is rounded to 16-bit types once (in fp16 under a power of two that
-    leaves 2^-38 of the largest gradient of a row as the least)."""
+    sum.  d, over the largest gradient of a row, is rounded to 16-bit types
+    once (in fp16 times 2^13, so that 2^-38 of that gradient is the least)."""
     dt = x.dtype
     D, V = x.shape[1], weight.shape[0]
     T = x.shape[0]
