@@ -30,6 +30,15 @@ namespace lapsum {
 
 constexpr int kNormWide = 1024;  // threads of a row that registers do not hold
 
+// (a launch counts its threads in 32 bits)
+static unsigned wide_grid(long long n) { return (unsigned)std::min(n, kGridMax / 4); }
+
+// The squares about a mean that was off by left / n, about the right one: in
+// their rounding where they cancel, infinite where they pass float32's range.
+LS_DEV float centred(float sq, float left, float inv) {
+    return sq < __builtin_inff() ? fmaxf(sq - left * (left * inv), 0.0f) : sq;
+}
+
 // Adds `a` and `b` over the NT threads that share a row.  s: LDS of the two
 // sums of every wave, taken in turn by `flip`, so that one barrier is enough.
 template <int NT>
@@ -173,7 +182,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* __restric
         }
         left = wave_sum_f32(left);
         mean = fmaf(left, inv, mean);
-        sq = fmaxf(wave_sum_f32(sq) - left * left * inv, 0.0f);
+        sq = centred(wave_sum_f32(sq), left, inv);
         row_moments<NT>(mean, sq, n, (float)D, s, count, flip);
         const float rstd = 1.0f / sqrtf(sq / (float)D + eps);
         if (tid == 0) {
@@ -219,9 +228,8 @@ __global__ __launch_bounds__(kNormWide) void k_norm_wide(const T* __restrict__ x
             }
         }
         row_sums<kNormWide>(sq, left, s, flip);
-        left /= (float)D;
-        mean += left;
-        sq = fmaxf(sq - left * left * (float)D, 0.0f);
+        mean += left / (float)D;
+        sq = centred(sq, left, 1.0f / (float)D);
         const float rstd = 1.0f / sqrtf(sq / (float)D + eps);
         if (threadIdx.x == 0) {
             if (mean_out) mean_out[r] = mean;
@@ -468,7 +476,7 @@ void launch_norm(const void* x, const void* weight, const void* bias, int dtype,
         with_shape<T>(D, [&](auto nt, auto u) {
             constexpr int NT = nt.value, U = u.value;
             if constexpr (NT == 0) {
-                hipLaunchKernelGGL((k_norm_wide<T, W>), dim3(grid_of(rows)), dim3(kNormWide), 0, st, (const T*)x,
+                hipLaunchKernelGGL((k_norm_wide<T, W>), dim3(wide_grid(rows)), dim3(kNormWide), 0, st, (const T*)x,
                                    (const W*)weight, (const W*)bias, rows, D, eps, (T*)y, mean, rstd);
             } else {
                 constexpr int kRows = NT < 256 ? 256 / NT : 1;
@@ -516,7 +524,7 @@ void launch_norm_vjp(const void* x, const void* weight, const float* mean, const
             constexpr int NT = nt.value, U = u.value;
             if constexpr (NT == 0) {
                 if (dx && rows > 0)
-                    hipLaunchKernelGGL((k_norm_vjp_wide<T, W>), dim3(grid_of(rows)), dim3(kNormWide), 0, st,
+                    hipLaunchKernelGGL((k_norm_vjp_wide<T, W>), dim3(wide_grid(rows)), dim3(kNormWide), 0, st,
                                        (const T*)x, (const W*)weight, mean, rstd, (const T*)dy, rows, D, (T*)dx);
                 if (part)
                     hipLaunchKernelGGL((k_norm_dw_wide<T>), dim3((unsigned)std::min(ceil_div(D, 256), 65535ll), (unsigned)n),
@@ -527,7 +535,7 @@ void launch_norm_vjp(const void* x, const void* weight, const float* mean, const
             }
         });
         if (part)
-            hipLaunchKernelGGL((k_norm_sum<W>), dim3(grid_of(ceil_div(D, 64)), 2), dim3(1024), 0, st, part, (int)n, D,
+            hipLaunchKernelGGL((k_norm_sum<W>), dim3(wide_grid(ceil_div(D, 64)), 2), dim3(1024), 0, st, part, (int)n, D,
                                (W*)dweight, (W*)dbias);
     });
 }

@@ -8,7 +8,8 @@ forward-mode tangents are refused, and so is torch.jit.trace); each gradient
 also has an entry point of its own (*_vjp).  They run in liblapsum.so
 (hand-written HIP for gfx950, the C ABI of include/lapsum_layers.h) on the
 caller's current stream, never wait for the device and can be captured into a
-graph.
+graph (of a backward pass, while no eager graph of the same leaves is alive:
+autograd would wait for those leaves' stream inside the capture).
 
 Rows may be float32, bfloat16 or float16.  Statistics and sums are held in
 float32 and rounded once to the rows' type.
@@ -64,7 +65,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor = None, bias: torch.Tensor 
 
     weight and bias have x's last dimension and either x's dtype or float32
     (both the same); None stands for 1 and 0.  Statistics are float32, the
-    variance from values about the mean."""
+    variance from values about the mean; one past float32's range is infinite,
+    and the row's result the bias."""
     _tensors(x=x)
     return _native().layer_norm(x, weight, bias, eps)
 
@@ -99,8 +101,9 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
 
     Differentiable with respect to x, weight and bias.  The logits are formed
     again for the gradient, a piece of the vocabulary at a time; their gradient,
-    over the largest of the rows' losses, is rounded once to the rows' type for
-    the products that follow, which hold their sums and the factor in float32."""
+    over the largest gradient of a row's loss, is rounded once to the rows' type
+    for the products that follow, which hold their sums and that factor in
+    float32."""
     _tensors(x=x, weight=weight, target=target)
     return _native().linear_cross_entropy(x, weight, target, bias, reduction)
 

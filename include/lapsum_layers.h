@@ -30,7 +30,8 @@ extern "C" {
  *   mean, rstd   : fp32[rows], what the VJP wants of the forward pass; each
  *                  may be NULL.
  * 0 <= rows <= LAPSUM_MAX_PAIRS, 1 <= width < 2^31, eps >= 0.  Statistics are
- * fp32, the variance from values about the mean.
+ * fp32, the variance from values about the mean; one past fp32's range is
+ * infinite, and y is the bias.
  */
 lapsum_status_t lapsum_layer_norm(const void* x, const void* weight, const void* bias, lapsum_dtype_t dtype,
                                   lapsum_dtype_t wtype, int64_t rows, int64_t width, float eps, void* y, float* mean,
@@ -72,8 +73,10 @@ lapsum_status_t lapsum_linear_cross_entropy(const void* x, const void* weight, c
                                             void* scratch, lapsum_stream_t stream);
 
 /*
- * With d = (e^(z - lse) - onehot) times the gradient of a row's loss, over the
- * largest such gradient rounded to dtype once: dx = d W, dweight = d^T x, dbias = the sum of d over the rows.
+ * With d = (e^(z - lse) - onehot) times the gradient of a row's loss: dx = d W,
+ * dweight = d^T x, dbias = the sum of d over the rows.  d is rounded to dtype
+ * once, over the largest gradient of a row's loss, which multiplies the fp32
+ * sums again.
  *   lse   : the forward's.
  *   dloss : fp32, the gradient of what the forward returned: [rows], or [1]
  *           with a reduction.  A row whose gradient is 0 adds nothing, whatever

@@ -115,6 +115,22 @@ def test_layer_norm_of_values_that_are_not_finite_stays_in_its_row():
         assert torch.equal(got[r], want[r]) if r in (0, 2, 5) else got[r].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [3, 300, 5000, 20000])
+def test_layer_norm_of_variances_past_float32(D, dtype):
+    """Squares of 1e24 are infinite, and so is the variance: the result is the bias, the gradient 0."""
+    x, w, b, dy = norm_case(4, D, dtype, dtype)
+    want = L.layer_norm(*put(x, w, b))
+    x[1], x[3] = torch.randn(2, D, generator=gen(2)).sign() * 1e24 + torch.randn(2, D, generator=gen(4)) * 1e23
+    y, mean, rstd = L.layer_norm_forward(*put(x, w, b))
+    dx, _, _ = L.layer_norm_vjp(*put(x, w), mean, rstd, dy.cuda())
+    for r in range(4):
+        if r in (0, 2):
+            assert torch.equal(y[r], want[r])
+        else:
+            assert torch.equal(y[r].cpu(), b) and rstd[r] == 0 and not dx[r].any()
+
+
 def test_layer_norm_of_other_strides_and_alignments():
     base = torch.randn(40, 130, generator=gen(3)).cuda()
     w, b = torch.rand(64, device="cuda"), torch.rand(64, device="cuda")
@@ -788,6 +804,85 @@ def test_graph_replays_follow_new_inputs(T, dtype):
         assert all(torch.equal(a, b) for a, b in zip(out, step())), i
 
 
+def training_step(x, p, plan):
+    """The gradients of fresh leaves through autograd, the experts' included."""
+    leaves = {k: t.detach().requires_grad_(True) for k, t in dict(p, x=x).items() if t.is_floating_point()}
+    rows = leaves["x"]
+    loss = model(rows, dict(p, **leaves), lambda h: plan)
+    return [loss.detach(), *torch.autograd.grad(loss, list(leaves.values()))]
+
+
+@pytest.mark.parametrize("T", [4, 700])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_replays_of_a_captured_backward_pass_follow_new_inputs(T, dtype):
+    """autograd's own pass through all of them, captured with the leaves made
+    inside the capture; every replay against the eager step."""
+    x, p, plan_of = model_inputs(T, dtype)
+    plan = plan_of(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            training_step(x, p, plan)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = training_step(x, p, plan)
+    for i in range(4):
+        x1, p1, _ = model_inputs(T, dtype, seed=10 + i)
+        for k in p:
+            p[k].copy_(p1[k])
+        x.copy_(x1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for j, (a, b) in enumerate(zip(out, training_step(x, p, plan))):
+            assert torch.equal(a, b), (i, j)
+
+
+def test_two_streams_at_once():
+    """Steps of two sizes, enqueued in turn on two streams, as each alone."""
+    cases = []
+    for T, dtype in ((60, torch.bfloat16), (500, torch.float32)):
+        x, p, plan_of = model_inputs(T, dtype)
+        cases.append((x, p, plan_of(x)))
+    want = [training_step(*c) for c in cases]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(6):
+        for c, side in zip(cases, sides):
+            with torch.cuda.stream(side):
+                got.append(training_step(*c))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2])), i
+
+
+def test_rows_that_are_the_vocabulary_too():
+    """One leaf in both places: its gradient is the sum of both."""
+    t = torch.randn(70, 40, generator=gen(6))
+    target = torch.arange(70).roll(3)
+    leaf = t.cuda().requires_grad_(True)
+    L.linear_cross_entropy(leaf, leaf, target.cuda(), reduction="sum").backward()
+    ref = R.loss(t, t, None, target, "sum", torch.ones(()))
+    (dx, dxe), (dw, dwe) = ref["dx"], ref["dw"]
+    X.check(leaf.grad, dx + dw, X.rounded(dx + dw, t.dtype, dxe + dwe), "gradient")
+
+
+def test_broadcast_inputs():
+    """A row that stands for many, and the scalar gradient of a sum: as the same
+    tensors laid out."""
+    row = torch.randn(1, 64, generator=gen(7)).cuda().requires_grad_(True)
+    one = torch.full((1,), 1.5, device="cuda", requires_grad=True)
+    v = torch.randn(30, 64, generator=gen(8)).cuda()
+    target = torch.arange(9, device="cuda")
+    L.linear_cross_entropy(L.layer_norm(row.expand(9, 64), one.expand(64)), v, target, reduction="none").sum().backward()
+    x, w = row.detach().repeat(9, 1).requires_grad_(True), one.detach().repeat(64).requires_grad_(True)
+    L.linear_cross_entropy(L.layer_norm(x, w), v, target, reduction="none").backward(torch.ones(9, device="cuda"))
+    assert torch.equal(row.grad, x.grad.sum(0, keepdim=True)) and torch.equal(one.grad, w.grad.sum(0, keepdim=True))
+
+
 # ---- offsets beyond 32 bits ---------------------------------------------------------
 
 @pytest.mark.slow
@@ -821,6 +916,20 @@ def test_norm_and_8_bits_past_2_to_the_31_elements():
     v = L.ScaledRows(part.values[3:].reshape(1, 3, D), part.scales[3:].reshape(1, 3, D // 128), D)
     three = L.expert_sort(torch.zeros(3, 1, dtype=torch.int32, device="cuda"), 1)
     assert torch.equal(ys[1:, at[3:] - T // 2], L.expert_linear_fp8(q3, v, three)[1:])
+
+
+@pytest.mark.slow
+def test_norm_of_a_row_of_more_columns_than_a_launch_has_threads_for():
+    """Sums of 2^28 columns' gradients leave in turns of the grid: of one row, dbias
+    is dy, and dweight dy times the normalised row."""
+    D = 2 ** 28 + 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, dy = (torch.empty(1, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    _, mean, rstd = L.layer_norm_forward(x)
+    _, dw, db = L.layer_norm_vjp(x, None, mean, rstd, dy, want=(False, True, True))
+    assert torch.equal(db, dy[0])
+    assert torch.equal(dw, (dy.float() * ((x.float() - mean) * rstd)).bfloat16()[0])
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.slow
