@@ -41,23 +41,22 @@ namespace lapsum {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
 
-constexpr int kStep8 = 64;  // k of one LDS buffer
-
-// One operand of a tile: R rows by kStep8 of k.  COLS: its rows are the
-// product's columns, dealt out to a fragment as above.
+// One operand of a tile: R rows by a block of k, 128 bytes of each.  COLS: its
+// rows are the product's columns, dealt out to a fragment as above.
 template <int R, bool COLS>
 struct Operand8 {
-    static constexpr int kBytes = R * 64;
-    static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads per step
+    static constexpr int kBytes = R * kBlock8;
+    static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads per block
 
     const char* base;  // the tile's first row
     uint32_t bytes;    // of the rows that exist
     uint32_t voff[kLoads];
 
-    // A row has 4 chunks of 16 bytes, two rows lie in a line of 128; a row's
-    // chunk c lies at c ^ fold(line).  Eight lanes that read one chunk of
-    // neighbouring fragment rows then meet no bank twice.
-    static LS_DEV int fold(int line) { return COLS ? (line & 1) | (line >> 2 & 2) : line & 3; }
+    // A row is a line of 128 bytes, whose chunk c of 16 lies at c ^ fold(row).
+    // LDS serves 256 bytes of such reads at a time: of the lanes 0-3, 12-15, 20-23
+    // and 24-27, then of 4-11, 16-19 and 28-31, and the same from 32 (measured, by
+    // pairs of lanes).  Of each sixteen the even rows have eight folds, and the odd.
+    static LS_DEV int fold(int row) { return row >> 1 & 7; }
 
     LS_DEV void init(const uint8_t* x, int own, uint32_t ld) {
         base = reinterpret_cast<const char*>(x);
@@ -65,15 +64,15 @@ struct Operand8 {
         const int l = lane_id(), w = uniform(threadIdx.x >> 6);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int line = (w * kLoads + i) * 8 + (l >> 3), u = (l & 7) ^ fold(line);
-            voff[i] = (uint32_t)(line * 2 + (u >> 2)) * ld + (u & 3) * 16;
+            const int row = (w * kLoads + i) * 8 + (l >> 3);
+            voff[i] = (uint32_t)row * ld + ((l & 7) ^ fold(row)) * 16;
         }
     }
-    // the buffer of k0 .. (empty past K: its loads write zeros)
-    LS_DEV u32x4 window(int k0, int K) const {
-        const char* p = base + k0;
-        return u32x4{(uint32_t)(uintptr_t)p, (uint32_t)((uintptr_t)p >> 32), k0 < K ? bytes - (uint32_t)k0 : 0u,
-                     0x00020000u};
+    // the buffer of block b (empty past the last: its loads write zeros)
+    LS_DEV u32x4 window(int b, int blocks) const {
+        const char* p = base + (size_t)b * kBlock8;
+        return u32x4{(uint32_t)(uintptr_t)p, (uint32_t)((uintptr_t)p >> 32),
+                     b < blocks ? bytes - (uint32_t)b * kBlock8 : 0u, 0x00020000u};
     }
     LS_DEV void load(const u32x4& win, uint32_t lds, int i) const {
         load_to_lds(win, voff[i], lds + (uniform(threadIdx.x >> 6) * kLoads + i) * 1024);
@@ -83,10 +82,10 @@ struct Operand8 {
         const int s = lane_id() & 31;
         return r0 + f * 32 + (COLS ? (s >> 2 & 1) * 16 + (s >> 3) * 4 + (s & 3) : s);
     }
-    // half h of it: chunk 2 (l / 32) + h of its row
-    static LS_DEV u32x4 half(const char* lds, int r0, int f, int h) {
-        const int r = row(r0, f), c = (lane_id() >> 5) * 2 + h;
-        return *(const u32x4*)(lds + (r >> 1) * 128 + (((r & 1) * 4 + c) ^ fold(r >> 1)) * 16);
+    // half h of it in step q of the block: chunk 4 q + 2 (l / 32) + h of its row
+    static LS_DEV u32x4 half(const char* lds, int r0, int f, int q, int h) {
+        const int r = row(r0, f), c = q * 4 + (lane_id() >> 5) * 2 + h;
+        return *(const u32x4*)(lds + r * kBlock8 + (c ^ fold(r)) * 16);
     }
 };
 
@@ -118,103 +117,91 @@ LS_DEV void expand(bf16x8 (&o)[2], u32x4 v, uint32_t scale) {
 }
 
 // EXACT: by the bf16 instruction
-template <int BM, int BN, bool EXACT>
+template <int B, bool EXACT>
 struct TileSums8 {
-    using OpA = Operand8<BM, false>;
-    using OpB = Operand8<BN, true>;
-    static constexpr int FM = BM / 64, FN = BN / 64;  // fragments of a wave
-    static constexpr int kBuffer = OpA::kBytes + OpB::kBytes;
-    static constexpr int kLds = kRing * kBuffer;
+    using OpA = Operand8<B, false>;
+    using OpB = Operand8<B, true>;
+    static constexpr int F = B / 64;  // fragments of a wave, of rows and of columns
+    static constexpr int kUnit = OpA::kBytes;
+    static constexpr int kLds = kRing * kUnit;
 
-    f32x16 acc[FM][FN] = {};
+    f32x16 acc[F][F] = {};
 
     // a, as: the tile's first row and its scales, M rows from there; b, bs, N
     // the same of its columns; left_a, left_b: scales from there to the array's end
     LS_DEV void run(const uint8_t* a, const uint8_t* as, int M, long long left_a, const uint8_t* b, const uint8_t* bs,
                     int N, long long left_b, int blocks, char* lds) {
         const int K = blocks * kBlock8, w = uniform(threadIdx.x >> 6);
-        const int r0 = (w >> 1) * (BM / 2), c0 = (w & 1) * (BN / 2);
+        const int r0 = (w >> 1) * (B / 2), c0 = (w & 1) * (B / 2);
         OpA oa;
         OpB ob;
         oa.init(a, M, (uint32_t)K);
         ob.init(b, N, (uint32_t)K);
-        u32x4 sa[FM], sb[FN];
+        u32x4 sa[F], sb[F];
         auto scales = [&](int blk) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
+            for (int i = 0; i < F; ++i) {
                 const long long at = (long long)min(OpA::row(r0, i), M - 1) * blocks;
                 sa[i] = scales16(as + at, blk, left_a - at);
             }
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
+            for (int j = 0; j < F; ++j) {
                 const long long at = (long long)min(OpB::row(c0, j), N - 1) * blocks;
                 sb[j] = scales16(bs + at, blk, left_b - at);
             }
         };
         const uint32_t at = (uint32_t)(uintptr_t)(LS_LDS(char)*)lds;
-        // steps s and s + 1 of one operand, interleaved, loads [from, to)
-        auto fetch = [&](const auto& op, const u32x4 (&win)[2], uint32_t to0, uint32_t to1, int from, int to) {
+        auto fetch = [&](const auto& op, const u32x4& win, int to, int from, int end) {
 #pragma unroll
-            for (int r = from; r < to; ++r) {
-                if (r & 1) op.load(win[1], to1, r >> 1);
-                else op.load(win[0], to0, r >> 1);
-            }
+            for (int i = from; i < end; ++i) op.load(win, at + to, i);
         };
+        // the units of the block that is multiplied, of the next, and a free one
+        int ua = 0, ub = kUnit, na = 2 * kUnit, nb = 3 * kUnit, spare = 4 * kUnit;
+        fetch(oa, oa.window(0, blocks), ua, 0, OpA::kLoads);
+        fetch(ob, ob.window(0, blocks), ub, 0, OpB::kLoads);
+        fetch(oa, oa.window(1, blocks), na, 0, OpA::kLoads);
+        fetch(ob, ob.window(1, blocks), nb, 0, OpB::kLoads);
+        u32x4 fa[2][F][2], fb[2][F][2];
+        step_barrier<OpA::kLoads + OpB::kLoads>();
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-            const int k0 = q * kStep8;
-            const u32x4 wa[2] = {oa.window(k0, K), oa.window(k0 + kStep8, K)};
-            const u32x4 wb[2] = {ob.window(k0, K), ob.window(k0 + kStep8, K)};
-            const uint32_t to = at + q * kBuffer;
-            fetch(oa, wa, to, to + kBuffer, 0, 2 * OpA::kLoads);
-            fetch(ob, wb, to + OpA::kBytes, to + OpA::kBytes + kBuffer, 0, 2 * OpB::kLoads);
-        }
-        u32x4 fa[2][FM][2], fb[2][FN][2];
-        step_barrier<2 * (OpA::kLoads + OpB::kLoads)>();
+        for (int f = 0; f < F; ++f)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fb[0][j][h] = OpB::half(lds + OpA::kBytes, c0, j, h);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fa[0][i][h] = OpA::half(lds, r0, i, h);
+            for (int h = 0; h < 2; ++h) {
+                fb[0][f][h] = OpB::half(lds + ub, c0, f, 0, h);
+                fa[0][f][h] = OpA::half(lds + ua, r0, f, 0, h);
+            }
         auto whole = [](const u32x4 (&f)[2]) {
             return __builtin_bit_cast(i32x8, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7));
         };
-        // as in the 16-bit tiles: step s multiplies the fragments of set s % 2
-        // and reads step s + 1 into the other; an even step fetches A for s + 4
-        // and s + 5, an odd one B for s + 3 and s + 4
-        int prev2 = 0, prev = 4 * kBuffer, cur = 0, next = kBuffer;
-        auto step = [&](auto qv, int k0) {
+        // Step q of block b multiplies the fragments of set q and reads the next
+        // step's into the other.  Step 0 fetches A of block b + 2 into the free
+        // unit.  Step 1, when all waves have read block b, waits for block b + 1
+        // and fetches B of block b + 2 to where A of b was; where its B was is free
+        // then.
+        auto step = [&](auto qv, int blk) {
             constexpr int q = decltype(qv)::value;
-            step_barrier<q == 0 ? 63 : 2 * OpA::kLoads>();
-            const char *pa = lds + next, *pb = pa + OpA::kBytes;
-            constexpr int kReads = 2 * (FM + FN), kReadIn = FM > 1 ? FM / 2 : 1;
-            const int kf = k0 + (q == 0 ? 4 : 3) * kStep8;
-            u32x4 win[2];
-            if (q == 0) win[0] = oa.window(kf, K), win[1] = oa.window(kf + kStep8, K);
-            else win[0] = ob.window(kf, K), win[1] = ob.window(kf + kStep8, K);
-            const uint32_t to0 = at + (q == 0 ? prev : prev2 + OpA::kBytes);
-            const uint32_t to1 = at + (q == 0 ? cur : prev + OpA::kBytes);
+            if (q) step_barrier<OpA::kLoads>();
+            const char *pa = lds + (q ? na : ua), *pb = lds + (q ? nb : ub);
+            constexpr int kReads = 4 * F, kReadIn = F > 1 ? F / 2 : 1;
+            const u32x4 win = q ? ob.window(blk + 2, blocks) : oa.window(blk + 2, blocks);
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
+            for (int i = 0; i < F; ++i) {
                 if (i < kReadIn) {
 #pragma unroll
                     for (int r = i * kReads / kReadIn; r < (i + 1) * kReads / kReadIn; ++r) {
                         const int f = r >> 1;
-                        if (f < FN) fb[q ^ 1][f][r & 1] = OpB::half(pb, c0, f, r & 1);
-                        else fa[q ^ 1][f - FN][r & 1] = OpA::half(pa, r0, f - FN, r & 1);
+                        if (f < F) fb[q ^ 1][f][r & 1] = OpB::half(pb, c0, f, q ^ 1, r & 1);
+                        else fa[q ^ 1][f - F][r & 1] = OpA::half(pa, r0, f - F, q ^ 1, r & 1);
                     }
                 }
-                if (q == 0) fetch(oa, win, to0, to1, i * 2 * OpA::kLoads / FM, (i + 1) * 2 * OpA::kLoads / FM);
-                else fetch(ob, win, to0, to1, i * 2 * OpB::kLoads / FM, (i + 1) * 2 * OpB::kLoads / FM);
+                if (q) fetch(ob, win, ua, i * OpB::kLoads / F, (i + 1) * OpB::kLoads / F);
+                else fetch(oa, win, spare, i * OpA::kLoads / F, (i + 1) * OpA::kLoads / F);
                 if constexpr (EXACT) {
                     bf16x8 a[2][2];
                     expand(a[0], fa[q][i][0], sa[i][0]);
                     expand(a[1], fa[q][i][1], sa[i][0]);
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) {
+                    for (int j = 0; j < F; ++j) {
                         bf16x8 b[2][2];
                         expand(b[0], fb[q][j][0], sb[j][0]);
                         expand(b[1], fb[q][j][1], sb[j][0]);
@@ -225,16 +212,12 @@ struct TileSums8 {
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < FN; ++j)
+                    for (int j = 0; j < F; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                             whole(fb[q][j]), whole(fa[q][i]), acc[i][j], 0, 0, 0, (int)sb[j][0], 0, (int)sa[i][0]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            prev2 = prev;
-            prev = cur;
-            cur = next;
-            next = next == (kRing - 1) * kBuffer ? 0 : next + kBuffer;
         };
         auto on = [](u32x4& s) {  // to the next block's scale
             s[0] = __builtin_amdgcn_alignbyte(s[1], s[0], 1);
@@ -248,15 +231,15 @@ struct TileSums8 {
             scales(b0);
             const int end = min(b0 + 16, blocks);
             for (int blk = b0; blk < end; ++blk) {
-                step(std::integral_constant<int, 0>{}, blk * kBlock8);
-                step(std::integral_constant<int, 1>{}, blk * kBlock8 + kStep8);
+                step(std::integral_constant<int, 0>{}, blk);
+                step(std::integral_constant<int, 1>{}, blk);
 #pragma unroll
-                for (int i = 0; i < FM; ++i) on(sa[i]);
-#pragma unroll
-                for (int j = 0; j < FN; ++j) on(sb[j]);
+                for (int f = 0; f < F; ++f) on(sa[f]), on(sb[f]);
+                const int free = ub;
+                ub = nb, nb = ua, ua = na, na = spare, spare = free;
             }
         }
-        // the last steps' loads, past K, still write zeros to LDS
+        // the last steps' loads, past the last block, still write zeros to LDS
         step_barrier<0>();
     }
 };
@@ -270,9 +253,9 @@ struct Piece8 {
     void* c;
     int M, N, blocks;  // blocks: 0 for unused rows
 };
-template <class T, int ACT, int BM, int BN>
+template <class T, int ACT, int B>
 LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
-    using Tile = TileSums8<BM, BN, sizeof(T) == 4>;
+    using Tile = TileSums8<B, sizeof(T) == 4>;
     Tile tile;
     const int M = p.M - i0, N = p.N - j0;
     if (p.blocks > 0) {
@@ -285,7 +268,7 @@ LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
     // of a row, its neighbours the next, so bias and activation are a short loop
     // and the stores are whole lines (unrolled over the registers: the same time
     // from ten times the code).
-    constexpr int WR = BM / 2, WC = BN / 2, V = 16 / (int)sizeof(T);
+    constexpr int WR = B / 2, WC = B / 2, V = 16 / (int)sizeof(T);
     constexpr int kLine = WC * 4 + 16;  // bytes of a row: neighbouring rows meet other banks
     constexpr int kPass = WR < 64 ? WR : 64;
     static_assert(4 * kPass * kLine <= Tile::kLds);
@@ -311,7 +294,7 @@ LS_DEV void tile8(const Piece8& p, int i0, int j0, char* lds) {
 #pragma unroll
         for (int i = 0; i < kPass / 32; ++i)
 #pragma unroll
-            for (int j = 0; j < Tile::FN; ++j)
+            for (int j = 0; j < Tile::F; ++j)
 #pragma unroll
                 for (int q = 0; q < 16; q += 4) {
                     const f32x16& a = tile.acc[pass / 32 + i][j];
@@ -355,7 +338,7 @@ template <class T, int ACT, int B>
 __global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g) {
     constexpr int kGroup = 4;  // row tiles that walk the columns together
     constexpr bool kCut = B == 256;
-    __shared__ __align__(1024) char lds[TileSums8<B, B, false>::kLds];
+    __shared__ __align__(1024) char lds[TileSums8<B, false>::kLds];
     const int cols = (g.out + B - 1) / B;
     RowTiles<B> rows(g.off, g.E, g.P);
     const Turn t = take_turn(blockIdx.x, rows.count() * cols, kCut);
@@ -382,11 +365,11 @@ __global__ __launch_bounds__(kProductThreads) void k_linear8(Linear8Args g) {
         if (t.quarter >= 0) {
             i0 += (t.quarter >> 1) * (B / 2);
             j0 += (t.quarter & 1) * (B / 2);
-            if (i0 < p.M && j0 < p.N) tile8<T, ACT, B / 2, B / 2>(p, i0, j0, lds);
+            if (i0 < p.M && j0 < p.N) tile8<T, ACT, B / 2>(p, i0, j0, lds);
             return;
         }
     }
-    tile8<T, ACT, B, B>(p, i0, j0, lds);
+    tile8<T, ACT, B>(p, i0, j0, lds);
 }
 
 void launch_expert_linear8(int dtype, const Linear8Args& g, hipStream_t st) {
