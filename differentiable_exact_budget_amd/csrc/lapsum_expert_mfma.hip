@@ -96,7 +96,7 @@ template <class T, int FORM, int ACT, int BM, int BN>
 __global__ __launch_bounds__(kProductThreads) void k_product(LinearArgs g) {
     constexpr int kGroup = 4;  // row tiles that walk the columns together: 4 x 8 tiles on an XCD at a time
     constexpr bool kCut = BM == 256;
-    __shared__ __align__(1024) char lds[kRing * (BM + BN) * kStepK * 2];
+    __shared__ __align__(1024) char lds[kRing * BM * kStepK * 2];
     const int cols = ((FORM == kFormY ? g.out : g.in) + BN - 1) / BN;
     Place<T> at;
     int quarter;

@@ -7,8 +7,8 @@
 
 namespace lapsum {
 
-constexpr int kStepK = 32;  // k of one LDS buffer
-constexpr int kRing = 5;    // LDS buffers
+constexpr int kStepK = 64;  // k of one LDS unit: two matrix instructions deep
+constexpr int kRing = 5;    // LDS units, each of one operand
 constexpr int kProductThreads = 256;
 
 // 16 bytes a lane from buffer offset `off` to LDS, lane l at `lds` + 16 l.
@@ -33,47 +33,50 @@ LS_DEV void step_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// One operand of a tile: R rows (of its own index) by kStepK of k.
+// One operand of a tile: R rows (of its own index) by kStepK of k, a unit.
+//   k contiguous: row i is a line of 128 bytes, a whole one of memory too (two
+//     steps of 64 bytes, fetched one after the other, waited for the line twice:
+//     products 3 to 6 % slower), whose chunk c of 16 bytes lies at c ^ fold(i).
+//     LDS serves 256 bytes of 16-byte reads at a time, of the lanes 0-3, 12-15,
+//     20-23 and 24-27, then of 4-11, 16-19 and 28-31, and the same from 32
+//     (measured, by pairs of lanes): the even rows of each sixteen reads meet
+//     eight places, and the odd.
+//   own index contiguous: two steps as StepLds lays them out.
 template <int R, bool KFAST, bool PAIRED>
-struct Operand : StepLds<R, KFAST, PAIRED> {
-    using Lds = StepLds<R, KFAST, PAIRED>;
-    using Lds::fold;
-    using Lds::kBytes;
-    static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads per step
-    static constexpr int kChunks = R / 8;                           // chunks of a k row (not KFAST)
+struct Operand {
+    using Step = StepLds<R, KFAST, PAIRED>;
+    static constexpr int kBytes = 2 * Step::kBytes;
+    static constexpr int kLoads = kBytes / (kProductThreads * 16);  // a wave's loads of a unit
+    static constexpr int kChunks = KFAST ? 8 : R / 8;               // chunks of a memory row
 
     const char* base;       // of the tile's first row and k
     uint32_t rows;          // rows of the tile that exist (KFAST), else its k
     uint32_t ld;            // bytes between rows of memory
     uint32_t last;          // not KFAST: bytes of the tile's last memory row that exist
-    uint32_t kcol;          // KFAST: first k of this lane's chunk
     uint32_t voff[kLoads];  // this lane's offsets
+    uint32_t kcol;          // KFAST: first k of this lane's chunk of load 0
 
+    static LS_DEV int fold(int i) {
+        if (!KFAST) return Step::fold(i);
+        return PAIRED ? (i >> 1 & 1) | (i >> 3 & 3) << 1 : i >> 1 & 7;
+    }
     // x: element (0, 0) of the tile; own: rows left of its own index; K:
     // length of the sum; ld_: elements between memory rows
     template <class T>
     LS_DEV void init(const T* x, int own, int K, int ld_) {
         base = reinterpret_cast<const char*>(x);
         ld = (uint32_t)ld_ * 2u;
+        rows = (uint32_t)(KFAST ? min(R, own) : K);
+        last = (uint32_t)min(R, own) * 2u;
         const int l = lane_id(), w = uniform(threadIdx.x >> 6);
-        if (KFAST) {
-            rows = (uint32_t)min(R, own);
-            const int u = (l & 7) ^ fold(l >> 3), c = u & 3;
-            kcol = c * 8;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                voff[i] = (uint32_t)((w * kLoads + i) * 16 + (l >> 3) * 2 + (u >> 2)) * ld + c * 16;
-        } else {
-            rows = (uint32_t)K;
-            last = (uint32_t)min(R, own) * 2u;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int k = (w * kLoads + i) * (64 / kChunks) + l / kChunks;
-                voff[i] = (uint32_t)k * ld + (uint32_t)((l % kChunks) ^ fold(k)) * 16;
-            }
+        for (int i = 0; i < kLoads; ++i) {
+            const int row = (w * kLoads + i) * (64 / kChunks) + l / kChunks, c = (l % kChunks) ^ fold(row);
+            voff[i] = (uint32_t)row * ld + (uint32_t)c * 16;
+            if (i == 0) kcol = c * 8;
         }
     }
-    // the buffer of k0 .. k0 + 31 (empty past K: its loads write zeros)
+    // the unit of k0 .. (empty past K: its loads write zeros)
     LS_DEV u32x4 window(int k0, int K) const {
         const char* p = base + (KFAST ? (size_t)k0 * 2 : (size_t)k0 * ld);
         uint32_t n = KFAST ? rows * ld - (uint32_t)k0 * 2
@@ -81,12 +84,21 @@ struct Operand : StepLds<R, KFAST, PAIRED> {
         if (k0 >= K) n = 0;
         return u32x4{(uint32_t)(uintptr_t)p, (uint32_t)((uintptr_t)p >> 32), n, 0x00020000u};
     }
-    // issues load i of the window into the LDS buffer at byte address `lds`
+    // issues load i of the window into the LDS unit at byte address `lds`
     LS_DEV void load(const u32x4& win, uint32_t lds, int i, int k0, int K) const {
         const int w = uniform(threadIdx.x >> 6);
-        // the last step of a sum: what follows in memory is the next row
-        const uint32_t off = KFAST && k0 + (int)kcol >= K ? 0x80000000u : voff[i];
+        // the last unit of a sum: what follows in memory is the next row
+        // (load i's rows differ from load 0's in these bits of their fold)
+        const int k = k0 + (int)(kcol ^ (PAIRED ? (i & 3) * 16 : (i & 1) * 32));
+        const uint32_t off = KFAST && k >= K ? 0x80000000u : voff[i];
         load_to_lds(win, off, lds + (w * kLoads + i) * 1024);
+    }
+    // fragment f, of the rows from r0, of step q of a unit
+    static LS_DEV s16x8 frag(const char* lds, int r0, int f, int q) {
+        if (!KFAST) return Step::frag(lds + q * Step::kBytes, r0, f);
+        const int l = lane_id(), i = l & 15;
+        const int row = r0 + (PAIRED ? (f >> 1) * 32 + (i >> 2) * 8 + (f & 1) * 4 + (i & 3) : f * 16 + i);
+        return *(const s16x8*)(lds + row * 128 + ((q * 4 + (l >> 4)) ^ fold(row)) * 16);
     }
 };
 
@@ -96,11 +108,12 @@ struct Operand : StepLds<R, KFAST, PAIRED> {
 // between memory rows.  All addresses and strides are on 16 bytes.
 template <class T, bool kA, bool kB, int BM, int BN>
 struct TileSums {
+    static_assert(BM == BN);  // the operands' units take each other's place
     using OpA = Operand<BM, kA, false>;
     using OpB = Operand<BN, kB, true>;
     static constexpr int FM = BM / 32, FN = BN / 32;  // fragments of a wave
-    static constexpr int kBuffer = OpA::kBytes + OpB::kBytes;
-    static constexpr int kLds = kRing * kBuffer;
+    static constexpr int kUnit = OpA::kBytes;
+    static constexpr int kLds = kRing * kUnit;
 
     f32x4 acc[FM][FN] = {};
 
@@ -113,73 +126,57 @@ struct TileSums {
         oa.init(a, own_a, K, lda);
         ob.init(b, own_b, K, ldb);
         const uint32_t at = (uint32_t)(uintptr_t)(LS_LDS(char)*)lds;
-        // steps s and s + 1 of one operand, interleaved, loads [from, to)
-        auto fetch = [&](const auto& op, const u32x4 (&win)[2], int k0, uint32_t to0, uint32_t to1, int from, int to) {
+        auto fetch = [&](const auto& op, const u32x4& win, int k0, int to, int from, int end) {
 #pragma unroll
-            for (int r = from; r < to; ++r) {
-                if (r & 1) op.load(win[1], to1, r >> 1, k0 + kStepK, K);
-                else op.load(win[0], to0, r >> 1, k0, K);
-            }
+            for (int i = from; i < end; ++i) op.load(win, at + to, i, k0, K);
         };
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-            const int k0 = q * kStepK;
-            const u32x4 wa[2] = {oa.window(k0, K), oa.window(k0 + kStepK, K)};
-            const u32x4 wb[2] = {ob.window(k0, K), ob.window(k0 + kStepK, K)};
-            const uint32_t to = at + q * kBuffer;
-            fetch(oa, wa, k0, to, to + kBuffer, 0, 2 * OpA::kLoads);
-            fetch(ob, wb, k0, to + OpA::kBytes, to + OpA::kBytes + kBuffer, 0, 2 * OpB::kLoads);
-        }
+        // the units of the k that are multiplied, of the next, and a free one
+        int ua = 0, ub = kUnit, na = 2 * kUnit, nb = 3 * kUnit, spare = 4 * kUnit;
+        fetch(oa, oa.window(0, K), 0, ua, 0, OpA::kLoads);
+        fetch(ob, ob.window(0, K), 0, ub, 0, OpB::kLoads);
+        fetch(oa, oa.window(kStepK, K), kStepK, na, 0, OpA::kLoads);
+        fetch(ob, ob.window(kStepK, K), kStepK, nb, 0, OpB::kLoads);
         s16x8 fa[2][FM], fb[2][FN];
-        step_barrier<2 * (OpA::kLoads + OpB::kLoads)>();
+        step_barrier<OpA::kLoads + OpB::kLoads>();
 #pragma unroll
-        for (int j = 0; j < FN; ++j) fb[0][j] = OpB::frag(lds + OpA::kBytes, c0, j);
+        for (int j = 0; j < FN; ++j) fb[0][j] = OpB::frag(lds + ub, c0, j, 0);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) fa[0][i] = OpA::frag(lds, r0, i);
-        // the buffers of steps s - 2, s - 1, s and s + 1
-        int prev2 = 0, prev = 4 * kBuffer, cur = 0, next = kBuffer;
-        // Step s multiplies the fragments of set s % 2 and reads step s + 1
-        // into the other.  An even step fetches A for s + 4 and s + 5, an odd
-        // one B for s + 3 and s + 4, into the two buffers whose fragments are
-        // all read.  An odd step waits for everything before the even step's
-        // loads: the buffers that it and the following step read.
+        for (int i = 0; i < FM; ++i) fa[0][i] = OpA::frag(lds + ua, r0, i, 0);
+        // Step q multiplies the fragments of set q and reads the next step's into
+        // the other.  Step 0 fetches A of two units on into the free unit.  Step 1,
+        // when all waves have read the present units, waits for the next ones and
+        // fetches B of two units on to where A was; where B was is free then.
         auto step = [&](auto qv, int k0) {
             constexpr int q = decltype(qv)::value;
-            step_barrier<q == 0 ? 63 : 2 * OpA::kLoads>();
-            const char *sa = lds + next, *sb = sa + OpA::kBytes;
+            if (q) step_barrier<OpA::kLoads>();
+            const char *sa = lds + (q ? na : ua), *sb = lds + (q ? nb : ub);
             constexpr int kReads = FM + FN, kReadIn = FM / 2;
-            const int kf = k0 + (q == 0 ? 4 : 3) * kStepK;
-            u32x4 win[2];
-            if (q == 0) win[0] = oa.window(kf, K), win[1] = oa.window(kf + kStepK, K);
-            else win[0] = ob.window(kf, K), win[1] = ob.window(kf + kStepK, K);
-            const uint32_t to0 = at + (q == 0 ? prev : prev2 + OpA::kBytes);
-            const uint32_t to1 = at + (q == 0 ? cur : prev + OpA::kBytes);
+            const int kf = k0 + 2 * kStepK;
+            const u32x4 win = q ? ob.window(kf, K) : oa.window(kf, K);
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 if (i < kReadIn) {
 #pragma unroll
                     for (int r = i * kReads / kReadIn; r < (i + 1) * kReads / kReadIn; ++r) {
-                        if (r < FN) fb[q ^ 1][r] = OpB::frag(sb, c0, r);
-                        else fa[q ^ 1][r - FN] = OpA::frag(sa, r0, r - FN);
+                        if (r < FN) fb[q ^ 1][r] = OpB::frag(sb, c0, r, q ^ 1);
+                        else fa[q ^ 1][r - FN] = OpA::frag(sa, r0, r - FN, q ^ 1);
                     }
                 }
-                if (q == 0) fetch(oa, win, kf, to0, to1, i * 2 * OpA::kLoads / FM, (i + 1) * 2 * OpA::kLoads / FM);
-                else fetch(ob, win, kf, to0, to1, i * 2 * OpB::kLoads / FM, (i + 1) * 2 * OpB::kLoads / FM);
+                if (q) fetch(ob, win, kf, ua, i * OpB::kLoads / FM, (i + 1) * OpB::kLoads / FM);
+                else fetch(oa, win, kf, spare, i * OpA::kLoads / FM, (i + 1) * OpA::kLoads / FM);
 #pragma unroll
                 for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<T>(fb[q][j], fa[q][i], acc[i][j]);
                 // keeps the compiler from gathering the loads
                 __builtin_amdgcn_sched_barrier(0);
             }
-            prev2 = prev;
-            prev = cur;
-            cur = next;
-            next = next == (kRing - 1) * kBuffer ? 0 : next + kBuffer;
         };
-        for (int k0 = 0; k0 < K; k0 += 2 * kStepK) {
+        for (int k0 = 0; k0 < K; k0 += kStepK) {
             step(std::integral_constant<int, 0>{}, k0);
-            step(std::integral_constant<int, 1>{}, k0 + kStepK);
+            step(std::integral_constant<int, 1>{}, k0);
+            const int free = ub;
+            ub = nb, nb = ua, ua = na, na = spare, spare = free;
         }
-        // the last steps' loads, past K, still write zeros to LDS
+        // the last loads, past K, still write zeros to LDS
         step_barrier<0>();
     }
     // f(row, column, eight sums from there) for what this lane holds: lane l has
