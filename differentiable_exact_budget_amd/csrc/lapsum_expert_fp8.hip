@@ -9,21 +9,24 @@
 //
 // The tiles are those of the 16-bit products (lapsum_tile_mfma.h): four waves,
 // a quarter of a B x B tile each, operands straight from memory to a ring of
-// five LDS buffers of 64 bytes of k.  A step is one matrix instruction deep (64
-// k), two steps are a block, and a row is whole blocks, so no load is masked
-// along the sum.
+// five LDS units, a block (128 bytes of k, a line of memory) of one operand
+// each.  A step is one matrix instruction deep (64 k), two steps are a block,
+// and a row is whole blocks, so no load is masked along the sum.
 //  - Scales stay in registers, 16 blocks' of each row that a lane multiplies,
 //    shifted on by a byte a block; the next 16 are fetched after 2048 k.
 //  - A weight fragment's rows are dealt out so that a lane's 16 sums of one
 //    row are 16 consecutive columns.
 //
-// 32768 rows, 8 experts 2048 -> 4096, bf16 results: 316 to 320 us (1.72 PFLOP/s; a
-// library's product of one such size, unscaled, 264), with silu 345, where the
-// 16-bit product takes 465 and 501; 4096 -> 4096: 546 us (2.0 PFLOP/s).  Of a
-// tile's 40 us the loop takes 31 (2.5 PFLOP/s; by the counters the matrix pipes
-// work 45 % of the time at 1.95 GHz, and 22 % of the requests miss the L2), its
-// first loads 3.5 and its results 5.5: all CUs write theirs at once, 33 MB, and
-// memory bounds that.  64 rows at 41 of 64 experts 2048 -> 1024, 86 MB: 18 us.
+// 32768 rows, 8 experts 2048 -> 4096, bf16 results: 306 to 315 us (1.77 PFLOP/s; a
+// library's product of one such size, unscaled, 264), with silu 332 to 342, where
+// the 16-bit product takes 459 and 480; 4096 -> 4096: 524 us (2.1 PFLOP/s).  Of a
+// tile's 39 us the loop takes 30, its first loads 3.5 and its results 5.5: all CUs
+// write theirs at once, 33 MB, and memory bounds that.  The loop is bound by its
+// feed, 10 TB/s: a sum of 32768 for 4096 x 4096 takes 448 us, 446 with a quarter of
+// its matrix instructions, 408 with all of them and operands that L2 always
+// holds (22 % of the requests miss it), 310 without loads (the matrix pipes' own
+// time, at 1.9 GHz).  More loads in flight, a third unit's, did not help: 508.
+// 64 rows at 41 of 64 experts 2048 -> 1024, 86 MB: 17 us.
 //
 // Accuracy.  Of eight neighbouring products that instruction drops what is 2^14
 // and more below the largest (measured: a product of 2^-13 of the largest is

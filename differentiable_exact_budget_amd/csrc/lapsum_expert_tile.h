@@ -2,7 +2,7 @@
 // how a step's operand lies in LDS (gfx950).
 //
 // A step is 64 bytes of k of R rows, laid out against bank conflicts in the
-// reads below (the hardware serves 128 bytes of LDS at a time).  The counters of
+// reads below (which lanes' reads meet: lapsum_tile_mfma.h).  The counters of
 // the 256-wide tiles show none where k is contiguous in both operands, and
 // conflicts in a third of the cycles that LDS indexes with one transposed
 // operand, in half of them with two:

@@ -35,8 +35,8 @@ LS_DEV void step_barrier() {
 
 // One operand of a tile: R rows (of its own index) by kStepK of k, a unit.
 //   k contiguous: row i is a line of 128 bytes, a whole one of memory too (two
-//     steps of 64 bytes, fetched one after the other, waited for the line twice:
-//     products 3 to 6 % slower), whose chunk c of 16 bytes lies at c ^ fold(i).
+//     steps of 64 bytes, each with a buffer of its own, asked for the line twice:
+//     the loss' forward tiles 1 to 2 % slower, 8-bit products 2 to 6 %), whose chunk c of 16 bytes lies at c ^ fold(i).
 //     LDS serves 256 bytes of 16-byte reads at a time, of the lanes 0-3, 12-15,
 //     20-23 and 24-27, then of 4-11, 16-19 and 28-31, and the same from 32
 //     (measured, by pairs of lanes): the even rows of each sixteen reads meet
