@@ -21,6 +21,7 @@
 // 576 us (119 TFLOP/s of 154).  513 rows of 257 over 1001 in fp32: kernels of 9 to
 // 12 us, the latencies of sums this short.
 #include "lapsum_layer_ops.h"
+#include "lapsum_rows.h"
 #include "lapsum_tile_any.h"
 
 namespace lapsum {
@@ -90,6 +91,7 @@ LossVjpPlan loss_any_plan(int dtype, const LossArgs& g) {
     p.shares = any_shares(dtype, g, p.width);
     size_t at = 0;
     p.g = take(at, ((size_t)g.T + 1) * 4);
+    p.x = take(at, (size_t)g.T * g.D * dtype_size(dtype));
     p.d = take(at, (size_t)g.T * p.width * dtype_size(dtype));
     if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
     p.bytes = at;
@@ -150,18 +152,24 @@ struct PutD {
         d[i * ld + j] = from_f<T>(gt == 0.0f ? 0.0f : (p - (target[i] == j0 + j ? 1.0f : 0.0f)) * gt);
     }
 };
+// (a row of dx whose g is 0 is 0, whatever the weights are)
 struct PutPart {
     float* c;
+    const float* g;
     long long ldc;
     bool add;
-    LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = add ? c[i * ldc + j] + v : v; }
+    LS_DEV void one(int i, int j, float v) const {
+        if (g[i] == 0.0f) v = 0.0f;
+        c[i * ldc + j] = add ? c[i * ldc + j] + v : v;
+    }
 };
 template <class T>
 struct PutOut {
     T* c;
+    const float* g;  // of dW: null
     long long ldc;
     float unscale;
-    LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = from_f<T>(v * unscale); }
+    LS_DEV void one(int i, int j, float v) const { c[i * ldc + j] = from_f<T>(g && g[i] == 0.0f ? 0.0f : v * unscale); }
 };
 // (eight at a time, one by one)
 template <class P>
@@ -182,10 +190,11 @@ struct AnyProduct {
     const float* unscale;  // of rows
     int shares;            // of K: partial sums, M * N elements apart
     bool add;
+    const float* g;        // of the rows, where c has a row for each
     // of logits
     const void* bias;
     const int64_t* target;
-    const float *lse, *g;
+    const float* lse;
     int v0, V;             // the piece's first column; the vocabulary
     float2* pairs;
     float* zt;
@@ -220,9 +229,9 @@ __global__ __launch_bounds__(kAnyThreads) void k_loss_any(AnyProduct g, long lon
         } else if constexpr (USE == kD) {
             sums(Each<PutD<T>>{{(T*)g.c + to, bias, target, g.lse + i0, g.g + i0, g.ldc, v0}, N});
         } else if constexpr (USE == kPartDx) {
-            sums(Each<PutPart>{{(float*)g.c + (long long)share * g.M * g.ldc + to, g.ldc, g.add}, N});
+            sums(Each<PutPart>{{(float*)g.c + (long long)share * g.M * g.ldc + to, g.g + i0, g.ldc, g.add}, N});
         } else {
-            sums(Each<PutOut<T>>{{(T*)g.c + to, g.ldc, *g.unscale}, N});
+            sums(Each<PutOut<T>>{{(T*)g.c + to, USE == kDx ? g.g + i0 : nullptr, g.ldc, *g.unscale}, N});
         }
         __syncthreads();
     }
@@ -389,19 +398,35 @@ void launch_loss_reduce(const LossArgs& g, const float* loss, int reduction, flo
 // ignored row; behind them what the products are multiplied by again.  One
 // workgroup.  So d is p - onehot itself where all rows have one gradient, and is
 // rounded row by row (times a common factor, the factor's rounding was in all
-// rows alike: up to 2^-9 of dx and dW in bf16).  SCALED (fp16): times 2^13,
-// which keeps small shares of the softmax above the type's least numbers.
-template <bool SCALED>
-__global__ __launch_bounds__(1024) void k_loss_grad_rows(const float* __restrict__ dloss, const int64_t* __restrict__ target,
-                                                         int T, int V, int reduction, float* __restrict__ g) {
+// rows alike: up to 2^-9 of dx and dW in bf16).  In fp16 times 2^13, which keeps
+// small shares of the softmax above the type's least numbers.
+//
+// The other workgroups copy x to `live` for dW's sums, with zeros in the rows
+// whose loss has no gradient: their d is 0, but 0 times what they hold is NaN
+// where that is not finite.  (A launch of their own took 3 us.)
+template <class T>
+__global__ __launch_bounds__(1024) void k_loss_grad_rows(LossArgs a, const float* __restrict__ dloss, int reduction,
+                                                         float* __restrict__ g, int packs, T* __restrict__ live) {
+    const auto on = [&](long long t) { return a.target[t] >= 0 && a.target[t] < a.V; };
+    const auto at = [&](long long t) { return dloss[reduction == kReduceNone ? t : 0]; };
+    if (blockIdx.x > 0) {
+        const long long n = (long long)packs * a.T;
+        for (long long i = (long long)(blockIdx.x - 1) * 1024 + threadIdx.x; i < n; i += (long long)(gridDim.x - 1) * 1024) {
+            const long long t = i / packs;
+            const int c = (int)(i - t * packs) * Pack<T>::V;
+            Pack<T> v{};
+            if (on(t) && at(t) != 0.0f) v = ld<false>((const T*)a.x + t * a.D, c, a.D);
+            st<T>(live + t * a.D, c, a.D, v);
+        }
+        return;
+    }
     __shared__ uint32_t s[16], c[16];
     uint32_t top = 0, count = 0;
-    for (int t = threadIdx.x; t < T; t += 1024) {
-        const bool on = target[t] >= 0 && target[t] < V;
-        count += on;
+    for (int t = threadIdx.x; t < a.T; t += 1024) {
+        count += on(t);
         // finite magnitudes, ordered as their bits
-        const uint32_t u = __float_as_uint(dloss[reduction == kReduceNone ? t : 0]) & 0x7FFFFFFFu;
-        if (on && u < 0x7F800000u) top = max(top, u);
+        const uint32_t u = __float_as_uint(at(t)) & 0x7FFFFFFFu;
+        if (on(t) && u < 0x7F800000u) top = max(top, u);
     }
     count = (uint32_t)wave_sum_u64(count);
     top = wave_max_u32(top);
@@ -411,19 +436,18 @@ __global__ __launch_bounds__(1024) void k_loss_grad_rows(const float* __restrict
     count = 0;
     for (int i = 0; i < 16; ++i) count += c[i];
     const float div = reduction == kReduceMean ? (float)max(count, 1u) : 1.0f;
-    const float most = top ? __uint_as_float(top) : 1.0f, scale = SCALED ? 8192.0f : 1.0f;
-    for (int t = threadIdx.x; t < T; t += 1024) {
-        const bool on = target[t] >= 0 && target[t] < V;
-        g[t] = on ? dloss[reduction == kReduceNone ? t : 0] / most * scale : 0.0f;
-    }
-    if (threadIdx.x == 0) g[T] = most / div / scale;
+    const float most = top ? __uint_as_float(top) : 1.0f, scale = std::is_same_v<T, _Float16> ? 8192.0f : 1.0f;
+    for (int t = threadIdx.x; t < a.T; t += 1024) g[t] = on(t) ? at(t) / most * scale : 0.0f;
+    if (threadIdx.x == 0) g[a.T] = most / div / scale;
 }
-void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int reduction, float* rows,
+void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int reduction, float* rows, void* live,
                            hipStream_t st) {
-    if (dtype == kF16)
-        hipLaunchKernelGGL(k_loss_grad_rows<true>, dim3(1), dim3(1024), 0, st, dloss, g.target, g.T, g.V, reduction, rows);
-    else
-        hipLaunchKernelGGL(k_loss_grad_rows<false>, dim3(1), dim3(1024), 0, st, dloss, g.target, g.T, g.V, reduction, rows);
+    with_dtype(dtype, [&](auto tv) {
+        using X = decltype(tv);
+        const long long packs = ceil_div(g.D, Pack<X>::V), n = live ? packs * g.T : 0;
+        hipLaunchKernelGGL(k_loss_grad_rows<X>, dim3((unsigned)(1 + std::min(ceil_div(n, 1024), 1ll << 16))), dim3(1024),
+                           0, st, g, dloss, reduction, rows, (int)packs, (X*)live);
+    });
 }
 
 // Column sums of a piece's d, 64 columns a workgroup: a wave adds every
@@ -511,6 +535,7 @@ void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, con
         AnyProduct q{};
         q.a = scratch + p.d;
         q.lda = p.ld;
+        q.g = rows;
         q.unscale = unscale;
         if (dx) {
             q.b = (const char*)g.w + (size_t)v0 * g.D * es;
@@ -522,7 +547,7 @@ void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, con
             else launch_any_product<kDx>(dtype, q, st);
         }
         if (dw) {
-            q.b = g.x;
+            q.b = scratch + p.x;
             q.M = n, q.N = g.D, q.K = g.T, q.ldb = g.D, q.ldc = g.D;
             q.c = (char*)dw + (size_t)v0 * g.D * es;
             q.shares = 1;

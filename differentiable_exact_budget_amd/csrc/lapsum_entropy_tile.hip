@@ -355,6 +355,7 @@ LossVjpPlan loss_tile_plan(const LossArgs& g) {
     p.shares = (int)std::max(1ll, std::min<long long>(512 / tiles, p.width / 512));
     size_t at = 0;
     p.g = take(at, ((size_t)g.T + 1) * 4);
+    p.x = take(at, (size_t)g.T * g.D * 2);
     p.d = take(at, (size_t)g.T * p.ld * 2);
     if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
     p.bytes = at;
@@ -427,6 +428,7 @@ struct LossProduct {
     int M, N, K, lda, ldb;
     int own_a;            // a's rows that can be read
     void* c;
+    const float* g;       // of dx's rows: those of a 0 are 0, whatever the weights are (of dW: null)
     const float* unscale;
     int shares;           // of K: partial sums, M * N elements apart
     int share;            // k of a share, a multiple of 64
@@ -442,8 +444,22 @@ LS_DEV void product_tile(const LossProduct& g, int i0, int j0, int z, char* lds)
     tile.run(a, g.own_a - i0, g.lda, b, N, g.ldb, K, lds);
     struct __attribute__((aligned(16))) T8 { T v[8]; };
     const float unscale = PART ? 1.0f : *g.unscale;
+    // kA: dx
+    constexpr int FM = BM / 32;
+    uint32_t none = 0;  // a bit a fragment
+    if constexpr (kA) {
+        const int r0 = (uniform(threadIdx.x >> 6) >> 1) * (BM / 2) + (lane_id() & 15);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) none |= (g.g[i0 + min(r0 + i * 16, M - 1)] == 0.0f ? 1u : 0u) << i;
+    }
     tile.each8([&](int row, int col, float (&v)[8]) {
         if (row >= M || col >= N) return;
+        if constexpr (kA) {
+            if (none >> (row >> 4 & (FM - 1)) & 1) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] = 0.0f;
+            }
+        }
         const long long to = (long long)(i0 + row) * g.N + j0 + col;
         if constexpr (PART) {
             f32x4* p = (f32x4*)((float*)g.c + (long long)z * g.M * g.N + to);
@@ -514,6 +530,7 @@ void launch_loss_tile_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, co
         LossProduct q{};
         q.a = scratch + p.d;
         q.lda = p.ld;
+        q.g = rows;
         q.unscale = unscale;
         if (dx) {
             q.b = (const char*)g.w + (size_t)v0 * g.D * 2;
@@ -525,7 +542,7 @@ void launch_loss_tile_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, co
             else launch_product<true, false>(dtype, q, st);
         }
         if (dw) {
-            q.b = g.x;
+            q.b = scratch + p.x;
             q.M = n, q.own_a = (n + 7) & ~7, q.N = g.D, q.K = g.T, q.ldb = g.D;
             q.c = (char*)dw + (size_t)v0 * g.D * 2;
             q.shares = 1;

@@ -118,7 +118,7 @@ lapsum_status_t lapsum_linear_cross_entropy_vjp(const void* x, const void* weigh
     char* s = static_cast<char*>(scratch);
     const bool tile = loss_tile_takes(dtype, g) && aligned16(dx) && aligned16(dweight);
     const LossVjpPlan p = tile ? loss_tile_plan(g) : loss_any_plan(dtype, g);
-    launch_loss_grad_rows(dtype, g, dloss, reduction, reinterpret_cast<float*>(s + p.g), st);
+    launch_loss_grad_rows(dtype, g, dloss, reduction, reinterpret_cast<float*>(s + p.g), dweight ? s + p.x : nullptr, st);
     if (tile) launch_loss_tile_vjp(dtype, g, p, lse, s, dx, dweight, dbias, st);
     else launch_loss_any_vjp(dtype, g, p, lse, s, dx, dweight, dbias, st);
     return launched();

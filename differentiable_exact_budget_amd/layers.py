@@ -95,7 +95,7 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
     x [..., width], weight [vocabulary, width] and bias [vocabulary] or None
     have one dtype; target [...] is int64.  A row whose target is outside [0,
     vocabulary) is ignored: its loss is 0, it has no gradient, and the mean does
-    not count it (and is 0 where no row counts).  reduction is "none", "sum" or
+    not count it (and is 0 where no row counts), whatever it holds.  reduction is "none", "sum" or
     "mean".  A bias of -inf takes an entry out of the vocabulary; a row with a
     logit of +inf or NaN, or with nothing but -inf, has a loss of NaN or inf.
 

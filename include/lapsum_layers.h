@@ -79,8 +79,9 @@ lapsum_status_t lapsum_linear_cross_entropy(const void* x, const void* weight, c
  * sums again.
  *   lse   : the forward's.
  *   dloss : fp32, the gradient of what the forward returned: [rows], or [1]
- *           with a reduction.  A row whose gradient is 0 adds nothing, whatever
- *           its logits are.
+ *           with a reduction.  A row that is ignored or whose gradient is 0
+ *           has a dx of 0 and adds nothing to dweight and dbias, whatever it
+ *           and its logits hold (infinities and NaN too).
  *   dx, dweight, dbias: dtype, shaped as x, weight, bias; each may be NULL.
  */
 size_t lapsum_linear_cross_entropy_vjp_scratch_bytes(lapsum_dtype_t dtype, int64_t rows, int64_t vocab,
