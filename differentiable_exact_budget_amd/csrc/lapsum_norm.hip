@@ -9,9 +9,15 @@
 // it in registers, U packs of 16 bytes each: it is read once, and its mean and
 // centred squares come from registers.  A wave takes the squares about its own
 // mean, and with them the sum of the differences, which is what the mean's
-// rounding left (so a row of one value has a variance of 0 and that mean); the
+// rounding left (so a row of one value has that mean, and its y is the bias); the
 // waves' counts, means and squares are merged afterwards, in one exchange
-// through LDS, and no squares of uncentred values are subtracted.  Workgroups walk the rows with the next row's loads in flight;
+// through LDS, and no squares of uncentred values are subtracted.  Values are
+// summed under a power of two, so the mean of finite values is finite; where the
+// sum of the squares passes float32's range, they are summed again under another,
+// so a variance is infinite only where it is past that range itself.  rstd and xh
+// are 0 then, and y is the bias.
+//
+// Workgroups walk the rows with the next row's loads in flight;
 // weight and bias stay in registers meanwhile, and so do the sums for their
 // gradients, which leave as one row of partial sums a workgroup.  k_norm_sum
 // adds those in their order: no atomics.
@@ -32,6 +38,20 @@ constexpr int kNormWide = 1024;  // threads of a row that registers do not hold
 
 // (a launch counts its threads in 32 bits)
 static unsigned wide_grid(long long n) { return (unsigned)std::min(n, kGridMax / 4); }
+
+// What values are summed times: those of a row in registers (2^14 at most), and of
+// any row (2^31); and those whose squares are summed again.
+constexpr float kDown = 0x1p-16f, kUp = 0x1p16f;
+constexpr float kDownWide = 0x1p-32f, kUpWide = 0x1p32f;
+constexpr float kDownSquares = 0x1p-84f, kUpSquares = 0x1p84f;
+
+// Whether sums over a row in registers can pass float32's range.
+template <class T>
+constexpr bool kFar = !std::is_same_v<T, _Float16>;
+
+// What a row's values are taken about once its variance is known: its mean, or 0
+// where rstd is 0 (differences from such a row's mean may be infinite).
+LS_DEV float about(float mean, float rstd) { return rstd == 0.0f ? 0.0f : mean; }
 
 // The squares about a mean that was off by left / n, about the right one: in
 // their rounding where they cancel, infinite where they pass float32's range.
@@ -79,8 +99,9 @@ LS_DEV void row_moments(float& mean, float& sq, float n, float D, float (*s)[2][
         const float first = s[flip][0][0];
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 1; i < NT / 64; ++i) sum = fmaf(s[flip][0][i] - first, count[i], sum);
-        mean = first + sum / D;
+        for (int i = 1; i < NT / 64; ++i)
+            sum = fmaf(s[flip][0][i] * 0.5f - first * 0.5f, count[i] * (2.0f * kDown), sum);
+        mean = fmaf(sum / D, kUp, first);
         sq = 0.0f;
 #pragma unroll
         for (int i = 0; i < NT / 64; ++i) {
@@ -159,8 +180,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* __restric
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += v[u][i];
-        float mean = wave_sum_f32(sum) * inv, sq = 0.0f, left = 0.0f;
+            for (int i = 0; i < V; ++i) sum = fmaf(v[u][i], kDown, sum);
+        float mean = wave_sum_f32(sum) * (inv * kUp), sq = 0.0f, left = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int n_u = min(max(held - u * V, 0), V);
@@ -181,14 +202,30 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* __restric
             }
         }
         left = wave_sum_f32(left);
-        mean = fmaf(left, inv, mean);
+        // (differences that overflow leave the mean as it is)
+        mean = !kFar<T> || fabsf(left) < __builtin_inff() ? fmaf(left, inv, mean) : mean;
         sq = centred(wave_sum_f32(sq), left, inv);
         row_moments<NT>(mean, sq, n, (float)D, s, count, flip);
-        const float rstd = 1.0f / sqrtf(sq / (float)D + eps);
+        float var = sq / (float)D;
+        // (the same for the row's threads)
+        if (kFar<T> && uniform(!(sq < __builtin_inff()))) {
+            float again = 0.0f, none = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = u * V + i < held ? fmaf(v[u][i], kDownSquares, -mean * kDownSquares) : 0.0f;
+                    again = fmaf(d, d, again);
+                }
+            row_sums<NT>(again, none, s, flip);
+            var = again / (float)D * kUpSquares * kUpSquares;
+        }
+        const float rstd = 1.0f / sqrtf(var + eps);
         if (tid == 0) {
             if (mean_out) mean_out[r] = mean;
             if (rstd_out) rstd_out[r] = rstd;
         }
+        if (kFar<T>) mean = about(mean, rstd);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             Pack<T> o;
@@ -214,10 +251,10 @@ __global__ __launch_bounds__(kNormWide) void k_norm_wide(const T* __restrict__ x
         for (long long c = (long long)threadIdx.x * V; c < D; c += kStep) {
             const Pack<T> p = ld<false>(row, c, D);
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += to_f(p.v[i]);
+            for (int i = 0; i < V; ++i) sum = fmaf(to_f(p.v[i]), kDownWide, sum);
         }
         row_sums<kNormWide>(sum, none, s, flip);
-        float mean = sum / (float)D, sq = 0.0f, left = 0.0f;
+        float mean = sum / (float)D * kUpWide, sq = 0.0f, left = 0.0f;
         for (long long c = (long long)threadIdx.x * V; c < D; c += kStep) {
             const Pack<T> p = ld<false>(row, c, D);
 #pragma unroll
@@ -228,13 +265,28 @@ __global__ __launch_bounds__(kNormWide) void k_norm_wide(const T* __restrict__ x
             }
         }
         row_sums<kNormWide>(sq, left, s, flip);
-        mean += left / (float)D;
+        if (fabsf(left) < __builtin_inff()) mean += left / (float)D;
         sq = centred(sq, left, 1.0f / (float)D);
-        const float rstd = 1.0f / sqrtf(sq / (float)D + eps);
+        float var = sq / (float)D;
+        if (!(sq < __builtin_inff())) {
+            float again = 0.0f;
+            for (long long c = (long long)threadIdx.x * V; c < D; c += kStep) {
+                const Pack<T> p = ld<false>(row, c, D);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = c + i < D ? fmaf(to_f(p.v[i]), kDownSquares, -mean * kDownSquares) : 0.0f;
+                    again = fmaf(d, d, again);
+                }
+            }
+            row_sums<kNormWide>(again, none, s, flip);
+            var = again / (float)D * kUpSquares * kUpSquares;
+        }
+        const float rstd = 1.0f / sqrtf(var + eps);
         if (threadIdx.x == 0) {
             if (mean_out) mean_out[r] = mean;
             if (rstd_out) rstd_out[r] = rstd;
         }
+        mean = about(mean, rstd);
         for (long long c = (long long)threadIdx.x * V; c < D; c += kStep) {
             const Pack<T> p = ld<false>(row, c, D);
             float w[V], b[V];
@@ -288,7 +340,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_vjp(const T* __res
     for (; r < rows; r += stride) {
         if (!kAhead) load(r), load_weights();
         float xh[U][V], g[U][V];
-        const float mean = nm, rstd = ns;
+        const float rstd = ns, mean = about(nm, rstd);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -358,7 +410,7 @@ __global__ __launch_bounds__(kNormWide) void k_norm_vjp_wide(const T* __restrict
     __shared__ float s[2][2][16];
     int flip = 0;
     for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
-        const float mean = mean_in[r], rstd = rstd_in[r];
+        const float rstd = rstd_in[r], mean = about(mean_in[r], rstd);
         float s1 = 0.0f, s2 = 0.0f;
         auto pass = [&](auto&& f) {
             for (long long c = (long long)threadIdx.x * V; c < D; c += kStep) {
@@ -401,7 +453,7 @@ __global__ __launch_bounds__(256) void k_norm_dw_wide(const T* __restrict__ x, c
 #pragma unroll 4
         for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
             const float d = to_f(dy[r * D + c]);
-            dw = fmaf(d, (to_f(x[r * D + c]) - mean_in[r]) * rstd_in[r], dw);
+            dw = fmaf(d, (to_f(x[r * D + c]) - about(mean_in[r], rstd_in[r])) * rstd_in[r], dw);
             db += d;
         }
         part[(long long)blockIdx.y * D + c] = dw;

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_layers import L, TYPES, gen, loss_case
+from test_gpu_layers import L, TYPES, check_norm, gen, loss_case, norm_case, put
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,51 @@ def test_rows_without_a_gradient_have_none_whatever_the_weights_hold(T, V, D, dt
     L.linear_cross_entropy(leaves[0], leaves[1], target.cuda(), bias=leaves[2]).backward()
     none = target < 0
     assert leaves[0].grad[none].abs().max() == 0 and leaves[0].grad[~none].isnan().any(1).all()
+
+
+# ---- norm rows whose sums pass float32's range ---------------------------------------
+
+# every shape of a row: a wave's, a workgroup's, and what registers do not hold
+WIDTHS = [2, 3, 300, 1001, 4096, 5000, 8192, 16384, 20001]
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_layer_norm_of_large_values_of_one_sign(dtype, D):
+    """Rows whose sum passes float32's range.  Of one value: the variance is 0 and
+    that value the mean, so y is the bias.  With a variance past the range: rstd is 0,
+    y the bias, and the gradient 0; the mean is as near as any sum of D.  The rows
+    between stay as they are."""
+    x, w, b, dy = norm_case(9, D, dtype, dtype)
+    want, mean0, rstd0 = L.layer_norm_forward(*put(x, w, b))
+    dx0, _, _ = L.layer_norm_vjp(*put(x, w), mean0, rstd0, dy.cuda())
+    big = torch.finfo(dtype).max
+    x[1], x[3] = 3e38, -big
+    x[5] = (2e38 * (1 + 0.2 * torch.randn(D, generator=gen(1)).clamp(-3, 3))).to(dtype)
+    x[7] = torch.where(torch.arange(D) % 3 == 0, -big, big).to(dtype)
+    y, mean, rstd = L.layer_norm_forward(*put(x, w, b))
+    dx, dw, db = L.layer_norm_vjp(*put(x, w), mean, rstd, dy.cuda())
+    assert dw.isfinite().all() and db.isfinite().all()
+    for r in range(9):
+        if r % 2 == 0:
+            assert torch.equal(y[r], want[r]) and torch.equal(dx[r], dx0[r])
+            assert mean[r] == mean0[r] and rstd[r] == rstd0[r]
+            continue
+        assert torch.equal(y[r].cpu(), b), r
+        true = float(x[r].double().mean())
+        if r < 4:
+            assert float(mean[r]) == true and abs(float(rstd[r]) - 1e-5 ** -0.5) < 1e-3
+        else:
+            depth = 64 + D / 1024  # of a row's sums
+            assert rstd[r] == 0 and not dx[r].any()
+            assert abs(float(mean[r]) - true) <= depth * 2.0 ** -24 * float(x[r].double().abs().mean())
+
+
+@pytest.mark.parametrize("D", [d for d in WIDTHS if d >= 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_layer_norm_of_variances_whose_sums_pass_float32(dtype, D):
+    """Values about 1.5e18: D squares are past float32's range, their mean is not."""
+    x, w, b, dy = norm_case(5, D, dtype, dtype)
+    x[1], x[4] = (1.5e18 * (torch.randn(2, D, generator=gen(2)) + 0.5)).to(dtype)
+    assert float(x[1].double().var()) * D > 3.5e38
+    check_norm(x, w, b, dy)
