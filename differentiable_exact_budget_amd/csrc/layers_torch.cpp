@@ -13,6 +13,11 @@ namespace {
 Tensor scratch_of(size_t bytes, const Tensor& like) {
     return bytes ? at::empty({(int64_t)bytes}, like.options().dtype(at::kByte)) : Tensor();
 }
+// whether a call has anything to write (what has no elements has no address)
+template <class... Tensors>
+bool written(const Tensors&... out) {
+    return ((out.defined() && out.numel() > 0) || ...);
+}
 Tensor laid_out(const Tensor& x) { return x.defined() ? x.contiguous() : x; }
 
 // rows of one of the three types, of any number of dimensions, at least one
@@ -72,7 +77,7 @@ std::tuple<Tensor, Tensor, Tensor> norm_vjp_call(const Tensor& x, const Tensor& 
     if (want[0]) dx = at::empty(dy.sizes(), dy.options());
     if (want[1]) dw = at::empty({width}, dy.options().dtype(wtype));
     if (want[2]) db = at::empty({width}, dy.options().dtype(wtype));
-    if (!want[0] && !want[1] && !want[2]) return {dx, dw, db};
+    if (!written(dx, dw, db)) return {dx, dw, db};
     if (want[1] || want[2]) scratch = scratch_of(lapsum_layer_norm_vjp_scratch_bytes(type_of(dy), rows, width), dy);
     check_ok(lapsum_layer_norm_vjp(ptr<void>(x), ptr<void>(weight), ptr<float>(mean), ptr<float>(rstd), ptr<void>(dy),
                                    type_of(dy), *row_type(wtype), rows, width, ptr<void>(dx), ptr<void>(dw),
@@ -181,7 +186,7 @@ std::tuple<Tensor, Tensor, Tensor> loss_vjp_call(const Tensor& x, const Tensor& 
     if (want[0]) dx = at::empty(x.sizes(), x.options());
     if (want[1]) dw = at::empty(weight.sizes(), weight.options());
     if (want[2]) db = at::empty({vocab}, weight.options());
-    if (!want[0] && !want[1] && !want[2]) return {dx, dw, db};
+    if (!written(dx, dw, db)) return {dx, dw, db};
     const Tensor scratch =
         scratch_of(lapsum_linear_cross_entropy_vjp_scratch_bytes(type_of(x), rows, vocab, width), x);
     check_ok(lapsum_linear_cross_entropy_vjp(ptr<void>(x), ptr<void>(weight), ptr<void>(bias), ptr<int64_t>(target),

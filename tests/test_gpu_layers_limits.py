@@ -106,3 +106,25 @@ def test_layer_norm_of_variances_whose_sums_pass_float32(dtype, D):
     x[1], x[4] = (1.5e18 * (torch.randn(2, D, generator=gen(2)) + 0.5)).to(dtype)
     assert float(x[1].double().var()) * D > 3.5e38
     check_norm(x, w, b, dy)
+
+
+# ---- gradients without elements --------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients_without_elements_are_empty(dtype):
+    """No rows, or no width, where those are the only gradients that are wanted."""
+    on = {"device": "cuda", "dtype": dtype}
+    x = torch.empty(0, 16, **on, requires_grad=True)
+    assert torch.autograd.grad(L.layer_norm(x).sum(), x)[0].shape == (0, 16)
+    y, mean, rstd = L.layer_norm_forward(x)
+    assert L.layer_norm_vjp(x, None, mean, rstd, y, want=(True, False, False))[0].shape == (0, 16)
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss = L.linear_cross_entropy(x, torch.rand(30, 16, **on), none)
+    assert torch.autograd.grad(loss, x)[0].shape == (0, 16)
+    e, w = torch.empty(5, 0, **on, requires_grad=True), torch.empty(30, 0, **on, requires_grad=True)
+    target = torch.arange(5, device="cuda")
+    dx, dw = torch.autograd.grad(L.linear_cross_entropy(e, w, target), (e, w))
+    assert dx.shape == (5, 0) and dw.shape == (30, 0)
+    _, lse = L.linear_cross_entropy_forward(e, w, target)
+    got = L.linear_cross_entropy_vjp(e, w, target, lse, torch.ones((), device="cuda"))
+    assert got[0].shape == (5, 0) and got[1].shape == (30, 0) and got[2] is None
