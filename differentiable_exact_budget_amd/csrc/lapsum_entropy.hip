@@ -12,10 +12,11 @@
 //
 // Here the products are those for any alignment (lapsum_tile_any.h).  Tiles of
 // 32 columns reduce them as they are; wide tiles' logits go through scratch in
-// fp32, a piece of the vocabulary at a time.  d is rounded to the rows'
-// type once, because the matrix instructions take it so; its rows are taken over
-// the largest gradient of a row's loss (k_loss_grad_rows), and the products are
-// multiplied by that again in fp32.
+// fp32, a piece of the vocabulary at a time.  For dx and dW d is rounded to the
+// rows' type once, because the matrix instructions take it so; its rows are taken
+// over the largest gradient of a row's loss (k_loss_grad_rows), and the products
+// are multiplied by that again in fp32.  db is summed before the rounding, by the
+// tiles that form d.
 //
 // fp32's matrix rate bounds the large ones: 4096 rows of 1024 over 8192, forward
 // 576 us (119 TFLOP/s of 154).  513 rows of 257 over 1001 in fp32: kernels of 9 to
@@ -93,6 +94,7 @@ LossVjpPlan loss_any_plan(int dtype, const LossArgs& g) {
     p.g = take(at, ((size_t)g.T + 1) * 4);
     p.x = take(at, (size_t)g.T * g.D * dtype_size(dtype));
     p.d = take(at, (size_t)g.T * p.width * dtype_size(dtype));
+    p.db = dtype == kF32 ? p.d : take(at, (size_t)ceil_div(g.T, 32) * 4 * p.width * 4);
     if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
     p.bytes = at;
     return p;
@@ -145,12 +147,21 @@ struct PutD {
     const int64_t* target;  // of the tile's first row
     const float *lse, *g;
     long long ld, j0;
-    LS_DEV void one(int i, int j, float v) const {
+    LS_DEV float value(int i, int j, float v) const {
         const float z = bias ? v + to_f(bias[j]) : v, gt = g[i];
         const float p = __builtin_amdgcn_exp2f((z - lse[i]) * kLog2e);
         // an ignored row has no gradient, whatever its logits are
-        d[i * ld + j] = from_f<T>(gt == 0.0f ? 0.0f : (p - (target[i] == j0 + j ? 1.0f : 0.0f)) * gt);
+        const float e = gt == 0.0f ? 0.0f : (p - (target[i] == j0 + j ? 1.0f : 0.0f)) * gt;
+        d[i * ld + j] = from_f<T>(e);
+        return e;
     }
+    LS_DEV void one(int i, int j, float v) const { value(i, j, v); }
+};
+// and its column sums, unrounded
+template <class T>
+struct PutDColumns : PutD<T> {
+    float* db;  // the tile's partial rows
+    LS_DEV void columns(int part, int j, float s) const { db[part * this->ld + j] = s; }
 };
 // (a row of dx whose g is 0 is 0, whatever the weights are)
 struct PutPart {
@@ -195,6 +206,7 @@ struct AnyProduct {
     const void* bias;
     const int64_t* target;
     const float* lse;
+    float* db;             // partial rows of d's column sums: 2 of a tile of rows, or 4 of a shared one; may be null
     int v0, V;             // the piece's first column; the vocabulary
     float2* pairs;
     float* zt;
@@ -227,7 +239,13 @@ __global__ __launch_bounds__(kAnyThreads) void k_loss_any(AnyProduct g, long lon
             static_assert(SPLIT && B == 32);
             sums(Each<PutPairs<T>>{{bias, target, v0, g.V, g.pairs + (long long)tj * g.M + i0, g.zt + i0}, N});
         } else if constexpr (USE == kD) {
-            sums(Each<PutD<T>>{{(T*)g.c + to, bias, target, g.lse + i0, g.g + i0, g.ldc, v0}, N});
+            const PutD<T> put{(T*)g.c + to, bias, target, g.lse + i0, g.g + i0, g.ldc, v0};
+            if constexpr (sizeof(T) == 2) {
+                if (g.db) sums(PutDColumns<T>{put, g.db + (long long)(i0 / B) * (SPLIT ? 4 : 2) * g.ldc + j0});
+                else sums(Each<PutD<T>>{put, N});
+            } else {
+                sums(Each<PutD<T>>{put, N});
+            }
         } else if constexpr (USE == kPartDx) {
             sums(Each<PutPart>{{(float*)g.c + (long long)share * g.M * g.ldc + to, g.g + i0, g.ldc, g.add}, N});
         } else {
@@ -450,17 +468,17 @@ void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int
     });
 }
 
-// Column sums of a piece's d, 64 columns a workgroup: a wave adds every
+// Column sums of a piece's partial rows, 64 columns a workgroup: a wave adds every
 // sixteenth row, and the waves' sums are added in wave order.
 template <class T>
-__global__ __launch_bounds__(1024) void k_loss_db(const T* __restrict__ d, int ld, int rows, int n,
+__global__ __launch_bounds__(1024) void k_loss_db(const float* __restrict__ part, int ld, int rows, int n,
                                                   const float* __restrict__ unscale, T* __restrict__ db) {
     __shared__ float s[16][64];
     const int l = lane_id(), w = uniform(threadIdx.x >> 6), c = blockIdx.x * 64 + l;
     float sum = 0.0f;
     if (c < n) {
 #pragma unroll 8
-        for (int t = w; t < rows; t += 16) sum += to_f(d[(long long)t * ld + c]);
+        for (int t = w; t < rows; t += 16) sum += part[(long long)t * ld + c];
     }
     s[w][l] = sum;
     __syncthreads();
@@ -468,10 +486,11 @@ __global__ __launch_bounds__(1024) void k_loss_db(const T* __restrict__ d, int l
     for (int i = 1; i < 16; ++i) sum += s[i][l];
     db[c] = from_f<T>(sum * *unscale);
 }
-void launch_loss_db(int dtype, const void* d, int ld, int T, int n, const float* unscale, void* db, hipStream_t st) {
+void launch_loss_db(int dtype, const float* part, int ld, int rows, int n, const float* unscale, void* db,
+                    hipStream_t st) {
     with_dtype(dtype, [&](auto tv) {
         using X = decltype(tv);
-        hipLaunchKernelGGL(k_loss_db<X>, dim3((unsigned)ceil_div(n, 64)), dim3(1024), 0, st, (const X*)d, ld, T, n,
+        hipLaunchKernelGGL(k_loss_db<X>, dim3((unsigned)ceil_div(n, 64)), dim3(1024), 0, st, part, ld, rows, n,
                            unscale, (X*)db);
     });
 }
@@ -530,8 +549,12 @@ void launch_loss_any_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, con
         AnyProduct z = any_piece(dtype, g, v0, n, scratch + p.d, p.ld);
         z.lse = lse;
         z.g = rows;
+        // (fp32's d is not rounded: its own rows)
+        z.db = db && dtype != kF32 ? (float*)(scratch + p.db) : nullptr;
         launch_any_product<kD>(dtype, z, st);
-        if (db) launch_loss_db(dtype, scratch + p.d, p.ld, g.T, n, unscale, (char*)db + (size_t)v0 * es, st);
+        const int side = any_side(dtype, g.T, n, 1);
+        const long long parts = dtype == kF32 ? g.T : ceil_div(g.T, side) * (side > 32 ? 2 : 4);
+        if (db) launch_loss_db(dtype, (const float*)(scratch + p.db), p.ld, (int)parts, n, unscale, (char*)db + (size_t)v0 * es, st);
         AnyProduct q{};
         q.a = scratch + p.d;
         q.lda = p.ld;

@@ -6,7 +6,8 @@
 // BN / 2 columns, and the target's logit is written by the lane that holds it.
 // Backward, the same tile becomes d, rounded to 16 bits, in scratch: a piece of
 // the vocabulary at a time, small enough that the products that follow, dx +=
-// d W and dW = d^T x, find it in the memory-side cache.
+// d W and dW = d^T x, find it in the memory-side cache.  db's sums are taken of d in
+// fp32, before that rounding: a wave's rows in registers, one partial row each.
 //
 // The products' feed bounds all of it (lapsum_tile_mfma.h), and beside a tile's
 // first loads and its exponentials no products run.  8192 rows of 2048 over 65536
@@ -208,7 +209,8 @@ template <class T, int FM, bool GRAD>
 __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, int v0, int n, float2* __restrict__ pairs,
                                                               float* __restrict__ zt, int ld,
                                                               const float* __restrict__ lse,
-                                                              const float* __restrict__ grad, T* __restrict__ d) {
+                                                              const float* __restrict__ grad, T* __restrict__ d,
+                                                              float* __restrict__ db) {
     constexpr int FN = kFewCols / 16, U = FM == 1 ? 4 : 2;  // steps of 32 k in flight
     constexpr int kPad = kFewCols + 4;
     __shared__ float part[kFewWaves][16][kPad];
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, int v0,
     }
     // lane l holds row l % 16 of a fragment, columns 4 (l / 16) .. + 3
     const int row = threadIdx.x >> 4, c = (threadIdx.x & 15) * 4;
-    float add[4];
+    float add[4], sums[4] = {};  // sums: of d over this thread's rows
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         add[r] = j0 + c + r >= n ? -__builtin_inff() : g.bias ? to_f(((const T*)g.bias)[v0 + j0 + c + r]) : 0.0f;
@@ -277,7 +279,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, int v0,
             for (int r = 0; r < 4; ++r) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(v[r] + add[r], kLog2e, lo));
                 const bool on = gt != 0.0f && j0 + c + r < n;
-                o.v[r] = from_f<T>(on ? (p - (at == r ? 1.0f : 0.0f)) * gt : 0.0f);
+                const float e = on ? (p - (at == r ? 1.0f : 0.0f)) * gt : 0.0f;
+                sums[r] += e;
+                o.v[r] = from_f<T>(e);
             }
             if (j0 + c < ld) *(T4*)(d + (long long)t * ld + j0 + c) = o;  // ld is a multiple of 8
             continue;
@@ -304,17 +308,25 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_loss_few(LossArgs g, int v0,
         if (at < 0 || at >= 4 || g.target[t] >= g.V) continue;
         zt[t] = at == 0 ? v[0] : at == 1 ? v[1] : at == 2 ? v[2] : v[3];
     }
+    if (!GRAD || !db) return;
+    // the wave's four rows of each sixteen: a partial row a wave
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        sums[r] += __uint_as_float(xor_lane<16>(__float_as_uint(sums[r])));
+        sums[r] += __uint_as_float(xor_lane<32>(__float_as_uint(sums[r])));
+    }
+    if (l < 16 && j0 + c < ld) *(f32x4*)(db + (long long)w * ld + j0 + c) = f32x4{sums[0], sums[1], sums[2], sums[3]};
 }
 
 template <bool GRAD>
 static void launch_few(int dtype, const LossArgs& g, int v0, int n, float2* pairs, float* zt, int ld, const float* lse,
-                       const float* grad, void* d, hipStream_t st) {
+                       const float* grad, void* d, float* db, hipStream_t st) {
     with_dtype(dtype, [&](auto tv) {
         using T = decltype(tv);
         if constexpr (sizeof(T) == 2) {
             auto launch = [&](auto fm) {
                 hipLaunchKernelGGL((k_loss_few<T, fm.value, GRAD>), dim3((unsigned)ceil_div(n, kFewCols)),
-                                   dim3(kFewWaves * 64), 0, st, g, v0, n, pairs, zt, ld, lse, grad, (T*)d);
+                                   dim3(kFewWaves * 64), 0, st, g, v0, n, pairs, zt, ld, lse, grad, (T*)d, db);
             };
             if (g.T <= 16) launch(std::integral_constant<int, 1>{});
             else launch(std::integral_constant<int, 2>{});
@@ -325,7 +337,7 @@ static void launch_few(int dtype, const LossArgs& g, int v0, int n, float2* pair
 void launch_loss_tile(int dtype, const LossArgs& g, const LossParts& p, char* scratch, hipStream_t st) {
     if (g.T <= kFewRows) {
         launch_few<false>(dtype, g, 0, g.V, (float2*)(scratch + p.pairs), (float*)(scratch + p.zt), 0, nullptr, nullptr,
-                          nullptr, st);
+                          nullptr, nullptr, st);
         return;
     }
     with_side(side_of(g.T, g.V), [&](auto bv) {
@@ -357,16 +369,20 @@ LossVjpPlan loss_tile_plan(const LossArgs& g) {
     p.g = take(at, ((size_t)g.T + 1) * 4);
     p.x = take(at, (size_t)g.T * g.D * 2);
     p.d = take(at, (size_t)g.T * p.ld * 2);
+    p.db = take(at, (size_t)std::max<long long>(2 * ceil_div(g.T, 64), kFewWaves) * p.ld * 4);
     if (p.pieces * p.shares > 1) p.dx = take(at, (size_t)p.shares * g.T * g.D * 4);
     p.bytes = at;
     return p;
 }
 
-// d of the columns v0 .. v0 + n - 1, zeros up to a multiple of 8
-template <class T, int B>
+// d of the columns v0 .. v0 + n - 1, zeros up to a multiple of 8, and with
+// DB: its column sums, unrounded, of each wave's rows: row 2 i + (0, 1) of db for row
+// tile i.  (As a choice at run time it cost those without a bias 1 %.)
+template <class T, int B, bool DB>
 __global__ __launch_bounds__(kProductThreads) void k_loss_dtile(LossArgs g, int v0, int n, int ld, int rows, int cols,
                                                                 const float* __restrict__ lse,
-                                                                const float* __restrict__ grad, T* __restrict__ d) {
+                                                                const float* __restrict__ grad, T* __restrict__ d,
+                                                                float* __restrict__ db) {
     using Tile = TileSums<T, true, true, B, B>;
     __shared__ __align__(1024) char lds[Tile::kLds];
     const TileAt at = tile_at(rows, cols, false);
@@ -395,30 +411,50 @@ __global__ __launch_bounds__(kProductThreads) void k_loss_dtile(LossArgs g, int 
         if (col >= ((N + 7) & ~7)) continue;
         float b[8] = {};
         add_bias(b, bias, col, N);
+        float sums[8] = {};
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i) {
             const int row = r0 + i * 16 + (l & 15);
             T8 o;
-            float p[8];
+            float p[8], e[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 float v = tile.acc[i][j + (r >> 2)][r & 3];
                 if (bias) v += b[r];
                 p[r] = __builtin_amdgcn_exp2f(fmaf(v, kLog2e, lo[i]));
                 // an ignored row has no gradient, whatever its logits are
-                o.v[r] = from_f<T>(gt[i] == 0.0f ? 0.0f : p[r] * gt[i]);
+                e[r] = gt[i] == 0.0f ? 0.0f : p[r] * gt[i];
             }
             if ((hit[i] & ~7) == in && gt[i] != 0.0f) {  // the target is here
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
-                    if (hit[i] == in + r) o.v[r] = from_f<T>((p[r] - 1.0f) * gt[i]);
+                    if (hit[i] == in + r) e[r] = (p[r] - 1.0f) * gt[i];
             }
+            if (DB && row < M) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) sums[r] += e[r];
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) o.v[r] = from_f<T>(e[r]);
             if (col + 8 > N) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
                     if (col + r >= N) o.v[r] = from_f<T>(0.0f);
             }
             if (row < M) *(T8*)(d + (long long)(i0 + row) * ld + j0 + col) = o;
+        }
+        if (!DB) continue;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {  // over the 16 lanes of these columns
+            sums[r] += __uint_as_float(xor_lane<8>(__float_as_uint(sums[r])));
+            sums[r] += __uint_as_float(xor_lane<4>(__float_as_uint(sums[r])));
+            sums[r] += __uint_as_float(xor_lane<2>(__float_as_uint(sums[r])));
+            sums[r] += __uint_as_float(xor_lane<1>(__float_as_uint(sums[r])));
+        }
+        if ((l & 15) == 0) {
+            f32x4* to = (f32x4*)(db + (long long)(at.i * 2 + (w >> 1)) * ld + j0 + col);
+            to[0] = f32x4{sums[0], sums[1], sums[2], sums[3]};
+            to[1] = f32x4{sums[4], sums[5], sums[6], sums[7]};
         }
     }
 }
@@ -515,18 +551,28 @@ void launch_loss_tile_vjp(int dtype, const LossArgs& g, const LossVjpPlan& p, co
     const bool part = p.pieces * p.shares > 1;
     for (int i = 0; i < p.pieces; ++i) {
         const int v0 = i * p.width, n = std::min(p.width, g.V - v0);
-        if (g.T <= kFewRows) launch_few<true>(dtype, g, v0, n, nullptr, nullptr, p.ld, lse, rows, scratch + p.d, st);
+        float* part_db = db ? (float*)(scratch + p.db) : nullptr;
+        long long db_rows = kFewWaves;
+        if (g.T <= kFewRows)
+            launch_few<true>(dtype, g, v0, n, nullptr, nullptr, p.ld, lse, rows, scratch + p.d, part_db, st);
         else with_side(side_of(g.T, n), [&](auto bv) {
             constexpr int B = bv.value;
             const long long r = ceil_div(g.T, B), c = ceil_div(n, B);
+            db_rows = 2 * r;
             with_dtype(dtype, [&](auto tv) {
                 using T = decltype(tv);
-                if constexpr (sizeof(T) == 2)
-                    hipLaunchKernelGGL((k_loss_dtile<T, B>), dim3((unsigned)turns(r * c, false)), dim3(kProductThreads),
-                                       0, st, g, v0, n, p.ld, (int)r, (int)c, lse, rows, (T*)(scratch + p.d));
+                auto launch = [&](auto sums) {
+                    hipLaunchKernelGGL((k_loss_dtile<T, B, sums.value>), dim3((unsigned)turns(r * c, false)),
+                                       dim3(kProductThreads), 0, st, g, v0, n, p.ld, (int)r, (int)c, lse, rows,
+                                       (T*)(scratch + p.d), part_db);
+                };
+                if constexpr (sizeof(T) == 2) {
+                    if (db) launch(std::true_type{});
+                    else launch(std::false_type{});
+                }
             });
         });
-        if (db) launch_loss_db(dtype, scratch + p.d, p.ld, g.T, n, unscale, (char*)db + (size_t)v0 * 2, st);
+        if (db) launch_loss_db(dtype, part_db, p.ld, (int)db_rows, n, unscale, (char*)db + (size_t)v0 * 2, st);
         LossProduct q{};
         q.a = scratch + p.d;
         q.lda = p.ld;

@@ -29,14 +29,15 @@ enum Reduction : int { kReduceNone = 0, kReduceSum = 1, kReduceMean = 2 };
 
 // The gradient's pieces of the vocabulary, and its scratch (all offsets in
 // bytes, each on 256): g[T] and its factor, x[T, D] of the rows that have a
-// gradient, d[T, ld] of one piece, dx's partial sums [shares, T, D] (where there
-// is more than one).
+// gradient, d[T, ld] of one piece, fp32 rows [, ld] whose sum is db's piece (d
+// before its rounding), dx's partial sums [shares, T, D] (where there is more than
+// one).
 struct LossVjpPlan {
     int width;   // columns of a piece
     int ld;      // elements between rows of d: the width on a multiple of 8
     int pieces;
     int shares;  // of dx's sum over a piece
-    size_t g, x, d, dx, bytes;
+    size_t g, x, d, db, dx, bytes;
 };
 
 // lapsum_entropy.hip: every type, width and alignment, and the steps around the
@@ -59,7 +60,9 @@ void launch_loss_reduce(const LossArgs& g, const float* loss, int reduction, flo
 // zeros for those without a gradient, to `live` (may be null)
 void launch_loss_grad_rows(int dtype, const LossArgs& g, const float* dloss, int reduction, float* rows, void* live,
                            hipStream_t st);
-void launch_loss_db(int dtype, const void* d, int ld, int T, int n, const float* unscale, void* db, hipStream_t st);
+// db of n columns from their partial rows
+void launch_loss_db(int dtype, const float* part, int ld, int rows, int n, const float* unscale, void* db,
+                    hipStream_t st);
 void launch_loss_dx(int dtype, const float* part, int shares, long long n, const float* unscale, void* dx,
                     hipStream_t st);
 

@@ -83,13 +83,22 @@ struct HasCell : std::false_type {};
 template <class P>
 struct HasCell<P, std::void_t<decltype(&P::cell)>> : std::true_type {};
 
+// whether a 16-bit output also wants sums over the rows (below)
+template <class P, class = void>
+struct HasColumns : std::false_type {};
+template <class P>
+struct HasColumns<P, std::void_t<decltype(&P::columns)>> : std::true_type {};
+
 // The sums over k < K of a(i, k) b(j, k) of a B x B tile; SPLIT: the waves share
 // the sum.  a, b: element (0, 0) of the tile; kA, kB: k is the contiguous index;
 // M, N: rows and columns that there are from there (1 and more); lda, ldb:
 // elements between memory rows.  put.one(i, j, v) takes a sum of the M x N,
 // put.eight(i, j, v) eight of a row, whose columns may pass N.  With SPLIT,
 // put.cell(i, j, v, on), if there is one, takes every place of the tile, B
-// neighbouring lanes a row of it, `on` where it is one of the M x N.
+// neighbouring lanes a row of it, `on` where it is one of the M x N.  put.columns,
+// if there is one, takes sums over rows of what put.value(i, j, v) makes of those
+// (and stores): columns(part, j, s), column j's over the rows of part 0 or 1 of the
+// tile, or with SPLIT 0 .. 3.
 template <class T, bool kA, bool kB, int B, bool SPLIT, class Put>
 LS_DEV void any_sums(const T* a, int M, int lda, const T* b, int N, int ldb, int K_, char* lds, const Put& put) {
     constexpr bool k16 = sizeof(T) == 2;
@@ -184,7 +193,30 @@ LS_DEV void any_sums(const T* a, int M, int lda, const T* b, int N, int ldb, int
     // Where a lane's sums lie: 16-bit, row l % 16 of fragment i and columns
     // 8 (l / 16) + 4 (j & 1) + r of the pair j / 2; fp32, rows
     // 8 (r / 4) + 4 (l / 32) + r % 4 and column l % 32
-    if constexpr (k16 && !SPLIT) {
+    if constexpr (k16 && !SPLIT && HasColumns<Put>::value) {
+#pragma unroll
+        for (int j = 0; j < F; j += 2) {
+            const int col = c0 + j * 16 + (l >> 4) * 8;
+            float s[8] = {};
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const int row = r0 + i * 16 + (l & 15);
+                if (row >= M) continue;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (col + r < N) s[r] += put.value(row, col + r, acc[i][j + (r >> 2)][r & 3]);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {  // over the 16 lanes of a column
+                s[r] += __uint_as_float(xor_lane<8>(__float_as_uint(s[r])));
+                s[r] += __uint_as_float(xor_lane<4>(__float_as_uint(s[r])));
+                s[r] += __uint_as_float(xor_lane<2>(__float_as_uint(s[r])));
+                s[r] += __uint_as_float(xor_lane<1>(__float_as_uint(s[r])));
+                if ((l & 15) == 0 && col + r < N) put.columns(w >> 1, col + r, s[r]);
+            }
+        }
+        return;
+    } else if constexpr (k16 && !SPLIT) {
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -216,13 +248,24 @@ LS_DEV void any_sums(const T* a, int M, int lda, const T* b, int N, int ldb, int
         float* part = reinterpret_cast<float*>(lds - w * 2 * kBuffer);
         each([&](int i, int j, float v) { part[(w * B + i) * kPad + j] = v; });
         __syncthreads();
+        static_assert(kAnyThreads % B == 0);  // a thread has one column
+        float s = 0.0f;
         for (int q = threadIdx.x; q < B * B; q += kAnyThreads) {
             const int i = q / B, j = q % B;
             float v = part[i * kPad + j];
 #pragma unroll
             for (int o = 1; o < 4; ++o) v += part[(o * B + i) * kPad + j];
-            if constexpr (HasCell<Put>::value) put.cell(i, j, v, i < M && j < N);
-            else if (i < M && j < N) put.one(i, j, v);
+            if constexpr (HasCell<Put>::value) {
+                put.cell(i, j, v, i < M && j < N);
+            } else if (i < M && j < N) {
+                if constexpr (HasColumns<Put>::value) s += put.value(i, j, v);
+                else put.one(i, j, v);
+            }
+        }
+        if constexpr (HasColumns<Put>::value) {
+            static_assert(B == 32);
+            s += __uint_as_float(xor_lane<32>(__float_as_uint(s)));
+            if (l < B && l < N) put.columns(w, l, s);
         }
     } else {
         each([&](int i, int j, float v) {

@@ -102,8 +102,8 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
     Differentiable with respect to x, weight and bias.  The logits are formed
     again for the gradient, a piece of the vocabulary at a time; their gradient,
     over the largest gradient of a row's loss, is rounded once to the rows' type
-    for the products that follow, which hold their sums and that factor in
-    float32."""
+    for the products that follow (x's and weight's gradients), which hold their
+    sums and that factor in float32; bias' is summed before that rounding."""
     _tensors(x=x, weight=weight, target=target)
     return _native().linear_cross_entropy(x, weight, target, bias, reduction)
 

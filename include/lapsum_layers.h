@@ -74,9 +74,9 @@ lapsum_status_t lapsum_linear_cross_entropy(const void* x, const void* weight, c
 
 /*
  * With d = (e^(z - lse) - onehot) times the gradient of a row's loss: dx = d W,
- * dweight = d^T x, dbias = the sum of d over the rows.  d is rounded to dtype
- * once, over the largest gradient of a row's loss, which multiplies the fp32
- * sums again.
+ * dweight = d^T x, dbias = the sum of d over the rows.  For dx and dweight d is
+ * rounded to dtype once, over the largest gradient of a row's loss, which
+ * multiplies the fp32 sums again; dbias is summed before that rounding.
  *   lse   : the forward's.
  *   dloss : fp32, the gradient of what the forward returned: [rows], or [1]
  *           with a reduction.  A row that is ignored or whose gradient is 0

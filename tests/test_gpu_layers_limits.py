@@ -6,6 +6,8 @@ import math
 import pytest
 import torch
 
+import expert_reference as X
+import layer_reference as R
 from test_gpu_layers import L, TYPES, check_norm, gen, loss_case, norm_case, put
 
 pytestmark = pytest.mark.gpu
@@ -128,3 +130,37 @@ def test_gradients_without_elements_are_empty(dtype):
     _, lse = L.linear_cross_entropy_forward(e, w, target)
     got = L.linear_cross_entropy_vjp(e, w, target, lse, torch.ones((), device="cuda"))
     assert got[0].shape == (5, 0) and got[1].shape == (30, 0) and got[2] is None
+
+
+# ---- the bias' gradient -----------------------------------------------------------------
+
+def check_db(x, w, b, target):
+    """db, whose sums are of d as it is in float32: what float32 rows may be off by,
+    and the result's rounding to its own type."""
+    leaves = [t.cuda() for t in (x, w, b)]
+    loss, lse = L.linear_cross_entropy_forward(leaves[0], leaves[1], target.cuda(), bias=leaves[2])
+    scale = torch.full((), 512.0 if x.dtype == torch.float16 else 1.0)
+    got = L.linear_cross_entropy_vjp(leaves[0], leaves[1], target.cuda(), lse, scale.cuda(), bias=leaves[2],
+                                     want=(True, True, True))
+    alone = L.linear_cross_entropy_vjp(leaves[0], leaves[1], target.cuda(), lse, scale.cuda(), bias=leaves[2],
+                                       want=(False, False, True))
+    assert torch.equal(alone[2], got[2])
+    fine = [t.float() for t in leaves]
+    db, tol = R.loss(fine[0], fine[1], fine[2], target.cuda(), "mean", scale.cuda())["db"]
+    X.check(got[2], db, X.rounded(db, x.dtype, tol), "db")
+
+
+@pytest.mark.parametrize("T,D", [(11, 64), (22, 64), (66, 64), (660, 72), (11, 33), (66, 33)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bias_gradients_that_cancel(dtype, T, D):
+    """Every entry of eleven has an eleventh of each row's softmax and is the target
+    of an eleventh of the rows: the gradient is 0, which sums of 1/11 and -10/11
+    rounded to 16 bits are not."""
+    x, w, b = torch.zeros(T, D, dtype=dtype), torch.ones(11, D, dtype=dtype), torch.zeros(11, dtype=dtype)
+    check_db(x, w, b, torch.arange(T) % 11)
+
+
+@pytest.mark.parametrize("T,V,D", [(30, 1000, 64), (300, 3001, 136), (3100, 4001, 64), (1100, 2100, 129), (90, 501, 33)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bias_gradients(dtype, T, V, D):
+    check_db(*loss_case(T, V, D, dtype))
