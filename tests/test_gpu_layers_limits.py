@@ -8,7 +8,7 @@ import torch
 
 import expert_reference as X
 import layer_reference as R
-from test_gpu_layers import L, TYPES, check_norm, gen, loss_case, norm_case, put
+from test_gpu_layers import L, TYPES, check_loss, check_norm, gen, loss_case, norm_case, put
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,82 @@ def test_bias_gradients_that_cancel(dtype, T, D):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_bias_gradients(dtype, T, V, D):
     check_db(*loss_case(T, V, D, dtype))
+
+
+# ---- the loss' rarer paths ------------------------------------------------------------
+
+CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def up256(n):
+    return -(-n // 256) * 256
+
+
+def tile_scratch(T, V, D):
+    """(pieces, scratch bytes) of the gradient's plan for 16-bit rows on 16 bytes."""
+    columns = lambda size: size // 2 // T // 256 * 256  # noqa: E731
+    fill = -(-(1 << 24) // (256 * D)) * 256
+    width = min(max(columns(256 << 20), min(fill, columns(1 << 30)), 256), 1 << 18, V)
+    ld, pieces = -(-width // 8) * 8, -(-V // width)
+    shares = max(1, min(512 // (-(-T // 64) * -(-D // 64)), width // 512))
+    size = up256((T + 1) * 4) + up256(T * D * 2) + up256(T * ld * 2) + up256(max(2 * -(-T // 64), 4) * ld * 4)
+    return pieces, size + (up256(shares * T * D * 4) if pieces * shares > 1 else 0)
+
+
+def any_scratch(T, V, D):
+    """The same of odd widths, with one share of a piece."""
+    width = min(max((128 << 20) // 4 // T // 128 * 128, 128), V)
+    pieces = -(-V // width)
+    size = up256((T + 1) * 4) + up256(T * D * 2) + up256(T * width * 2) + up256(-(-T // 32) * 16 * width)
+    return pieces, size + (up256(T * D * 4) if pieces > 1 else 0)
+
+
+def loss_in_chunks(x, w, b, target, dloss, rows):
+    """The gradients of a mean and their tolerances, `rows` rows at a time: those of
+    dw and db with a rounding for every chunk."""
+    count = max(1, int(((target >= 0) & (target < w.shape[0])).sum()))
+    dx, dw, db = [], 0, 0
+    for r in range(0, x.shape[0], rows):
+        ref = R.loss(x[r:r + rows], w, b, target[r:r + rows], "sum", dloss / count)
+        dx.append(torch.stack(ref["dx"]))
+        dw, db = dw + torch.stack(ref["dw"]), db + torch.stack(ref["db"])
+    return torch.cat(dx, 1), dw, db
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:])
+@pytest.mark.parametrize("T,V,D,scratch", [(524_003, 2500, 8, tile_scratch), (200_003, 300, 9, any_scratch)])
+def test_gradients_in_three_pieces_of_the_vocabulary(dtype, T, V, D, scratch):
+    """Every piece with a share of each row's softmax, and the last one ragged."""
+    pieces, size = scratch(T, V, D)
+    assert pieces == 3
+    assert L.layers.lib().lapsum_linear_cross_entropy_vjp_scratch_bytes(CODE[dtype], T, V, D) == size
+    x, w, b, target = put(*loss_case(T, V, D, dtype, drop=0.5))
+    leaves = [t.requires_grad_(True) for t in (x, w, b)]
+    dloss = torch.full((), 1024.0 if dtype == torch.float16 else 1.0, device="cuda")
+    loss = L.linear_cross_entropy(x, w, target, bias=b)
+    got = torch.autograd.grad(loss, leaves, dloss)
+    for name, a, (value, tol) in zip(("dx", "dw", "db"), got, loss_in_chunks(
+            x.detach(), w.detach(), b.detach(), target, dloss, 50_000)):
+        X.check(a, value, tol, name)
+
+
+# odd widths on wide tiles; the widest tiles of the forward pass and of d over several
+# steps, and with a last round cut into quarters, one of which has no columns; the
+# widest of dx (cut, in two pieces) and of dw
+@pytest.mark.parametrize("T,V,D", [(1100, 2100, 129), (4096, 3601, 200), (1024, 16465, 72), (16_700, 17_000, 1024)])
+@pytest.mark.parametrize("dtype", TYPES[1:])
+def test_losses_on_wide_tiles(dtype, T, V, D):
+    check_loss(*put(*loss_case(T, V, D, dtype)), on="cuda")
+
+
+def test_odd_rows_off_16_bytes_on_wide_tiles():
+    """Widths of whole 16 bytes at an address that is not."""
+    x, w, b, target = loss_case(1100, 2100, 128, torch.bfloat16)
+    want = check_loss(x, w, b, target, on="cuda")
+    off = [torch.cat([t.new_zeros(1), t.reshape(-1)]).cuda()[1:].reshape(t.shape).requires_grad_(True) for t in (x, w, b)]
+    assert off[0].data_ptr() % 16 == 2
+    L.linear_cross_entropy(off[0], off[1], target.cuda(), bias=off[2]).backward(torch.rand((), generator=gen(5)).cuda() + 0.5)
+    ref = R.loss(*(t.cuda() for t in (x, w, b, target)), "mean", torch.rand((), generator=gen(5)).cuda() + 0.5)
+    for name, t, u in zip(("dx", "dw", "db"), off, want):
+        X.check(t.grad, *ref[name], name)
+        assert t.grad.shape == u.grad.shape
