@@ -11,9 +11,10 @@
 //
 // The products' feed bounds all of it (lapsum_tile_mfma.h), and beside a tile's
 // first loads and its exponentials no products run.  8192 rows of 2048 over 65536
-// in bf16: forward 1.70 to 1.76 ms (1.25 to 1.29 PFLOP/s; a library's product 1.2 to
-// 1.44), gradients 5.16 ms, in pieces of 16384 columns d 0.47, dx and dW 0.41 each
-// (1.33 PFLOP/s).  4096 rows of 1024 over 50001 in fp16: forward 387 us.
+// in bf16: forward 1.69 to 1.76 ms (1.25 to 1.30 PFLOP/s; a library's product 1.2 to
+// 1.44), gradients 5.05 to 5.35 ms, in pieces of 16384 columns d 0.47, dx and dW 0.40
+// each (1.37 PFLOP/s).  4096 rows of 1024 over 50001 in fp16 with a bias: the forward
+// call 411 to 437 us, its gradients 1500.
 #include "lapsum_layer_ops.h"
 #include "lapsum_tile_mfma.h"
 

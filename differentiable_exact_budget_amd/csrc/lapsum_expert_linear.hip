@@ -12,8 +12,8 @@
 //  - Few tiles: 32 x 32 a workgroup, and its four waves split the sum, each on
 //    its own in its own part of LDS; their results are added in wave order.
 // 32768 x 2047 rows -> 4095 in bf16: y 1.07 ms (0.51 PFLOP/s), dx 0.91 (0.59),
-// dW 0.82 (0.65), bound by the way through registers; 32768 x 2048 -> 4096 in
-// fp32: y 4.76 ms (116 TFLOP/s), dx 4.72, dW 4.41, the matrix instruction's
+// dW 0.88 (0.62), bound by the way through registers; 32768 x 2048 -> 4096 in
+// fp32: y 4.08 ms (135 TFLOP/s), dx 4.14, dW 4.31, the matrix instruction's
 // rate being 157.
 #include <algorithm>
 

@@ -11,30 +11,31 @@
 // A workgroup of four waves forms a BM x BN tile of C, each wave a quarter of
 // it: with 256 x 256 a wave holds 128 x 128 fp32 sums in 256 registers, the
 // most there is, so a byte that is brought to LDS is used as often as it can
-// be.  The sum runs in steps of 32 k, one matrix instruction deep.
+// be.  The main loop (lapsum_tile_mfma.h) takes 64 of k of one operand as a unit,
+// two steps of one matrix instruction each.
 //  - Operands go from memory to LDS without passing through registers
-//    (buffer_load ... lds, 16 bytes a lane) into a ring of five buffers.  Two
-//    steps are fetched as one, alternately all of A and all of B, so that the
-//    two halves of a 128-byte line are asked for together, and the loads are
-//    spread evenly between the matrix instructions: a wave that issues many
-//    at once stands still until the memory pipeline has taken them.
+//    (buffer_load ... lds, 16 bytes a lane) into a ring of five units: those of A
+//    and B that are multiplied, the next ones, and a free one.  A step fetches one
+//    operand's unit, whole 128-byte lines of it where k is contiguous, and the
+//    loads are spread evenly between the matrix instructions: a wave that issues
+//    many at once stands still until the memory pipeline has taken them.
 //  - While a step's fragments are multiplied, the next step's are read from
-//    LDS into a second set of registers.
+//    LDS into a second set of registers.  The waves meet once in two steps.
 //  - Reads out of range return zero, which is all the masking that ragged
 //    experts need: a tile's buffer ends with its expert's last row.
 //
-// 32768 rows, 8 experts 2048 -> 4096 in bf16 (0.55 TFLOP): y 0.50 ms, 1.1
-// PFLOP/s; dx 0.47, dW 0.44.  What bounds it is the feed: the loads to LDS
-// alone, without a product, take 0.41 / 0.38 / 0.37 ms; the matrix instructions
-// alone would take 0.36.  By the counters the matrix pipes work 44 / 54 / 51 %
-// of the time (y with silu, dx, dW) and 32 / 25 / 21 % of the requests miss the
-// L2.  A tile's first loads and its epilogue stand alone, no products beside
-// them: an activation adds what its instructions take (silu 16 us to y's 500,
-// gelu 46), and short sums feel it most: 16384 rows, 16 experts 1024 -> 4096 in
-// f16 (0.14 TFLOP, 96 us at a large product's rate) take 160 us without one,
-// 169 with silu, 189 with gelu.
+// 32768 rows, 8 experts 2048 -> 4096 in bf16 (0.55 TFLOP): y 0.45 ms, 1.2
+// PFLOP/s; dx 0.43, dW 0.43.  Feed and products bound it together: the loads to
+// LDS alone, without reads and products, take 0.36 / 0.30 / 0.30 ms (with what
+// the tiles write), all but the loads 0.31 / 0.34 / 0.33.  By the counters the
+// matrix pipes work 46 / 57 / 53 % of the time (y with silu, dx, dW) and 32 / 25 /
+// 21 % of the requests miss the L2.  A tile's first loads and its epilogue stand
+// alone, no products beside them: an activation adds what its instructions take
+// (silu 16 us to y's 453, gelu 48), and short sums feel it most: 16384 rows, 16
+// experts 1024 -> 4096 in f16 (0.14 TFLOP, 96 us at a large product's rate) take
+// 138 us without one, 150 with silu, 166 with gelu.
 //
-// A wave's direct-to-LDS store is 64 consecutive chunks of the step's layout
+// A wave's direct-to-LDS store is 64 consecutive chunks of a unit's layout
 // in LDS, so the layout's permutation is made on the global side: each lane
 // fetches the chunk that belongs at its place.  B's fragments come in pairs
 // that share 32 columns, so a lane ends with 8 consecutive columns of a row of
@@ -153,22 +154,22 @@ bool expert_mfma_takes(int form, int dtype, const LinearArgs& g) {
 }
 
 // The tile's side, by what was measured (bf16, 64 / 128 / 256, us; R: rows of
-// an expert on average; tiles: of 256, the row forms' taken as half filled at
-// each expert's end):
-//   y, 64 experts 2048 -> 1024, R = 1:      30 / 32 / 48    (few rows: more
-//                               R = 16:     45 / 46 / 53    workgroups stream
-//                               R = 64:     85 / 64 / 68    the weights)
-//   y, 8 experts 2048 -> 2048, 160 tiles:   69 / 55 / 58
-//                              288 tiles:  124 / 84 / 81
-//   y, 64 experts 512 -> 1024, 384 tiles:   47 / 37 / 49    (a short sum)
-//   dx, 8 experts 2048 -> 1024, 32 tiles:   20 / 23 / 29
-//   dW, 8 experts, 512 x 512, 32 tiles:     17 / 21 / 21
-//       8 experts, 2048 x 1024, 256 tiles:  21 / 19 / 18
-//       64 experts, 1024 x 2048, R = 1:     79 / 65 / 73
+// an expert on average, here of each):
+//   y, 64 experts 2048 -> 1024, R = 1:      39 / 40 / 45    (few rows: more
+//                               R = 16:     39 / 41 / 46    workgroups stream
+//                               R = 64:     54 / 48 / 53    the weights)
+//   y, 8 experts 2048 -> 2048, R = 512:     56 / 34 / 43
+//                              R = 1024:   106 / 64 / 56
+//   y, 64 experts 512 -> 1024, R = 256:     38 / 27 / 26    (a short sum)
+//   dx, 8 experts 2048 -> 1024, R = 25:    9.3 / 11 / 15
+//                               R = 512:    33 / 22 / 30
+//   dW, 8 experts, 512 x 512, R = 512:     6.1 / 7.7 / 9.2
+//       8 experts, 2048 x 1024, R = 512:    33 / 24 / 23
+//       64 experts, 1024 x 2048, R = 1:     83 / 69 / 73
 // R takes the experts without rows in, so rows that are all one expert's among
 // many get too small a tile: 4096 rows 1024 -> 128, y 58 us as one of 1024
 // experts and 8 as the only one.  And dW's sum is never split over workgroups:
-// 65536 rows of 4 experts 64 -> 64 take 83 us on 4 of them, their bytes 3.
+// 65536 rows of 4 experts 64 -> 64 take 58 us on 4 of them, their bytes 3.
 static int tile_side(int form, const LinearArgs& g) {
     const long long per = g.P / g.E;
     if (form == kFormDw) {
@@ -182,11 +183,12 @@ static int tile_side(int form, const LinearArgs& g) {
 
 void launch_expert_mfma(int form, int dtype, const LinearArgs& g, hipStream_t st) {
     // Few rows for each expert, or few at all: without LDS.  64-wide tiles / few,
-    // us, weights in the memory-side cache and from memory: 64 experts
-    // 2048 -> 1024, 1 row of an expert 27 / 29 and 44 / 33, 2 rows 35 / 36 and
-    // 57 / 42, 4 rows 38 / 43 and 64 / 51, 8 rows 40 / 51 and 65 / 62; 8 experts
-    // 2048 -> 4096, 2 rows 20 / 18 and 31 / 21; 64 experts 512 -> 1024, 4 rows
-    // 13 / 15 and 15 / 18; 16 experts 512 -> 512, 4 rows 5.7 / 4.1 and 6.8 / 4.4.
+    // us, weights in the memory-side cache (as far as it holds them) and from
+    // memory, every expert with rows: 64 experts 2048 -> 1024, 1 row of an expert
+    // 38 / 39 and 63 / 46, 2 rows 39 / 41 and 63 / 48, 4 rows 39 / 44 and 64 / 52, 8
+    // rows 39 / 50 and 64 / 62; 8 experts 2048 -> 4096, 2 rows 21 / 22 and 33 / 26;
+    // 64 experts 512 -> 1024, 4 rows 12 / 15 and 15 / 19; 16 experts 512 -> 512, 4
+    // rows 5.5 / 4.0 and 8.1 / 4.8.
     const bool few = (g.in >= 1024 && g.P <= 4 * g.E) || g.P * ceil_div(g.out, 64) < 1024;
     if (form == kFormY && few && expert_few_takes(g)) {
         launch_expert_few(dtype, g, st);

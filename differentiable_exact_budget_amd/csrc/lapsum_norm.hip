@@ -25,10 +25,11 @@
 // Statistics, sums and partial sums are fp32.  The row's own rounding to 16
 // bits happens once, at the store.
 //
-// Memory bounds it: 16384 rows of 4096 in bf16 with fp32 weights, 268 MB, 55 us
-// (4.9 TB/s); its gradients, 403 MB, 77 us (5.2 TB/s) of which k_norm_sum is 7.
-// 1000 rows of 1001 in fp32: 4.7 and 10 us, latencies of a row's loads and of the
-// sums after each other.
+// Memory bounds it: 16384 rows of 4096 in bf16 with fp32 weights, 268 MB, 49 to 55
+// us back to back (4.9 to 5.5 TB/s); its gradients, 403 MB, 70 to 77 us (5.2 to 5.8
+// TB/s) of which k_norm_sum is 5 to 7.  1000 rows of 1001 in fp32: 4.8 and 10 us,
+// latencies of a row's loads and of the sums after each other.  2000 rows of 32768 in
+// bf16, past registers: 151 us (131 MB read three times and written) and 254.
 #include "lapsum_layer_ops.h"
 #include "lapsum_rows.h"
 
